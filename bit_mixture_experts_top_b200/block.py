@@ -1,0 +1,140 @@
+"""The dense operators of a block around the routed 4-bit layer, on one GPU.
+
+Thin owners of device buffers around the C ABI, as :mod:`layer` is for the
+routed layer: :class:`RmsNorm` (the layer's input from the hidden stream, and
+its backward) and :class:`GradClipper` (the gradients that the backward calls
+leave).  Nothing here computes.
+
+Every call runs on the current stream of the tensors' device.  Outputs and
+workspaces are allocated per call from torch's allocator, so calls on several
+streams, and calls captured into several graphs, share nothing.
+"""
+import torch
+
+from . import e4b
+
+
+def _check(t, name, shape, *dtypes):
+    """A contiguous CUDA tensor of this shape and one of these types, or ValueError."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"e4b: {name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError(f"e4b: {name} must be {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)}, "
+                         f"got {t.dtype} of {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"e4b: {name} must be contiguous")
+    return t
+
+
+class _On:
+    """Makes the tensors' device the current one for a call; all of them must be on it."""
+
+    def __init__(self, *tensors):
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1:
+            raise ValueError(f"e4b: tensors on several devices: {sorted(map(str, devices))}")
+        self.device = devices.pop()
+        self.guard = None if self.device.index == torch.cuda.current_device() else torch.cuda.device(self.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.device
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+class RmsNorm:
+    """Root-mean-square norm of a hidden stream [T, H] (bf16) with the residual's addition in the same pass.
+
+    r = bf16(x + residual) (x itself without a residual), y = r * rstd * weight."""
+
+    def __init__(self, weight: torch.Tensor, eps=1e-6):
+        if weight.dim() != 1 or weight.numel() < 1:
+            raise ValueError("e4b: weight must be [H]")
+        self.H, self.eps = weight.numel(), float(eps)
+        self.weight = _check(weight, "weight", (self.H,), torch.bfloat16)
+
+    def _run(self, x, residual, q_format, want_rstd):
+        if x.dim() != 2:
+            raise ValueError("e4b: x must be [T, H]")
+        T, H = x.shape[0], self.H
+        _check(x, "x", (T, H), torch.bfloat16)
+        if residual is not None:
+            _check(residual, "residual", (T, H), torch.bfloat16)
+        with _On(x, residual, self.weight) as dev:
+            r = x if residual is None else torch.empty_like(x)
+            y = q = scales = None
+            if q_format == e4b.E4B_Q8_NONE:
+                y = torch.empty_like(x)
+            else:
+                q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
+                scales = torch.empty((T,), dtype=torch.float32, device=dev) if q_format == e4b.E4B_Q8_ROW else \
+                    torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
+            rstd = torch.empty((T,), dtype=torch.float32, device=dev) if want_rstd else None
+            e4b.e4b_rmsnorm(x, residual, self.weight, T, H, self.eps, q_format, r if residual is not None else None, y,
+                            q, scales, rstd)
+        return y, q, scales, r, rstd
+
+    def forward(self, x, residual=None):
+        """(y [T, H] bf16, r [T, H] bf16): the normed rows and the new stream (x itself without a residual)."""
+        y, _, _, r, _ = self._run(x, residual, e4b.E4B_Q8_NONE, False)
+        return y, r
+
+    def forward_q8(self, x, residual=None, scales="mx"):
+        """(q [T, H] float8_e4m3fn, scales, r): the normed rows in 8 bits.  scales "mx": E8M0 bytes [T, H / 32] (uint8),
+        value = q * 2^(byte - 127); "row": fp32 [T], value = q * scale."""
+        if scales not in ("mx", "row"):
+            raise ValueError(f"e4b: scales must be 'mx' or 'row', got {scales!r}")
+        _, q, s, r, _ = self._run(x, residual, e4b.E4B_Q8_MX if scales == "mx" else e4b.E4B_Q8_ROW, False)
+        return q, s, r
+
+    def forward_train(self, x, residual=None):
+        """(y, r, rstd [T] fp32): the forward with what :meth:`backward` needs."""
+        y, _, _, r, rstd = self._run(x, residual, e4b.E4B_Q8_NONE, True)
+        return y, r, rstd
+
+    def backward(self, dy, r, rstd, dr=None):
+        """(dx [T, H] bf16, dweight [H] fp32) from dy [T, H] (fp32 or bf16) and, with dr [T, H] bf16, the gradient that
+        reaches the stream r directly.  dx is the gradient of x and of the residual alike."""
+        if r.dim() != 2:
+            raise ValueError("e4b: r must be [T, H]")
+        T, H = r.shape[0], self.H
+        _check(r, "r", (T, H), torch.bfloat16)
+        _check(rstd, "rstd", (T,), torch.float32)
+        _check(dy, "dy", (T, H), torch.float32, torch.bfloat16)
+        if dr is not None:
+            _check(dr, "dr", (T, H), torch.bfloat16)
+        with _On(dy, r, rstd, dr, self.weight) as dev:
+            dx = torch.empty_like(r)
+            dw = torch.empty((H,), dtype=torch.float32, device=dev)
+            ws = torch.empty(e4b.e4b_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
+            e4b.e4b_rmsnorm_backward(dy, e4b.DTYPES[dy.dtype], dr, r, self.weight, rstd, T, H, dx, dw, ws)
+        return dx, dw
+
+
+class GradClipper:
+    """Clipping of a fixed list of gradient tensors (fp32, bf16 and fp16 mixed, each contiguous) by their global norm.
+
+    The list is described once and its tensors are held; every :meth:`clip` reads them anew."""
+
+    def __init__(self, grads, out=None):
+        """out: tensors of the same types and sizes that take the clipped values; None clips in place."""
+        self.grads = e4b.make_grads(grads, out)
+        everything = [t for ts in self.grads.tensors for t in ts]
+        if not everything:
+            raise ValueError("e4b: no gradient tensors")
+        with _On(*everything) as dev:
+            self.device = dev
+
+    def clip(self, max_norm):
+        """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before clipping, a 0-d fp32
+        tensor on the device.  max_norm float("inf"): the norm alone."""
+        with _On(self.grads.tensors[0][0]) as dev:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+            ws = torch.empty(e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads)), dtype=torch.uint8, device=dev)
+            e4b.e4b_clip_grad_norm(self.grads, float(max_norm), norm, ws)
+        return norm

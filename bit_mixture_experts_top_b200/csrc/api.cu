@@ -2,8 +2,10 @@
 // sequence of the layer forward (route -> gather -> gate_up -> down -> combine).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
 
 #include "e4b.h"
 #include "e4b_device.cuh"
@@ -180,6 +182,20 @@ KernelChoice pick_kernel(const e4b_moe_desc& d, int32_t T) {
   if (avg <= 96) return {false, 128};
   return {false, 256};
 }
+
+// A byte range of device memory, for the overlap checks of calls that allow some buffers to coincide.
+struct Range {
+  uintptr_t lo, hi;
+};
+
+Range range_of(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, p ? a + bytes : a};
+}
+
+bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+bool same_or_apart(const Range& a, const Range& b) { return !overlap(a, b) || (a.lo == b.lo && a.hi == b.hi); }
 
 template <typename T>
 T* at(void* base, size_t off) {
@@ -542,6 +558,129 @@ e4b_status e4b_moe_backward(const e4b_moe_desc* d, int32_t T, const uint16_t* lo
   b.lora_A = lora_A;
   b.lora_B = lora_B;
   return launch_moe_backward(b, reinterpret_cast<cudaStream_t>(stream));
+}
+
+e4b_status e4b_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                       double eps, int32_t q_format, uint16_t* r_out, uint16_t* y, uint8_t* q, void* q_scales,
+                       float* rstd, e4b_stream stream) {
+  if (T < 0 || H < 1 || !(eps >= 0.0) || !std::isfinite(eps)) return E4B_ERR_INVALID_ARG;
+  if (q_format != E4B_Q8_NONE && q_format != E4B_Q8_ROW && q_format != E4B_Q8_MX) return E4B_ERR_INVALID_ARG;
+  if (q_format == E4B_Q8_MX && H % 32 != 0) return E4B_ERR_UNSUPPORTED;
+  if (T == 0) return E4B_OK;
+  const bool quant = q_format != E4B_Q8_NONE;
+  if (!x || !weight || (q != nullptr) != quant || (q_scales != nullptr) != quant || (!y && !q) || (r_out && !residual))
+    return E4B_ERR_INVALID_ARG;
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(r_out, 2) || !aligned(y, 2) ||
+      !aligned(rstd, 4) || (q_format == E4B_Q8_ROW && !aligned(q_scales, 4)))
+    return E4B_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(T) * H;
+  const Range in[3] = {range_of(x, 2 * n), range_of(residual, 2 * n), range_of(weight, 2 * static_cast<size_t>(H))};
+  const Range out[5] = {range_of(r_out, 2 * n), range_of(y, 2 * n), range_of(q, n),
+                        range_of(q_scales, q_format == E4B_Q8_ROW ? 4 * static_cast<size_t>(T) : n / 32),
+                        range_of(rstd, 4 * static_cast<size_t>(T))};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (i < 2 && j < 2 ? !same_or_apart(out[i], in[j]) : overlap(out[i], in[j])) return E4B_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return E4B_ERR_INVALID_ARG;
+  }
+  const NormLaunch p{x, residual, weight, T, H, 1.0 / H, eps, q_format, r_out, y, q, q_scales, rstd};
+  return launch_rmsnorm(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
+}
+
+size_t e4b_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H) {
+  if (T < 0 || H < 1) return 0;
+  return align_up(static_cast<size_t>(norm_backward_blocks(T)) * H * 4);
+}
+
+e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t* dr, const uint16_t* r,
+                                const uint16_t* weight, const float* rstd, int32_t T, int32_t H, uint16_t* dx,
+                                float* dweight, void* ws, size_t ws_bytes, e4b_stream stream) {
+  if (T < 0 || H < 1 || (dy_type != E4B_F32 && dy_type != E4B_BF16)) return E4B_ERR_INVALID_ARG;
+  if (!dweight || !aligned(dweight, 4)) return E4B_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
+  if (!dy || !r || !weight || !rstd || !dx || !ws || !aligned(ws, kAlign)) return E4B_ERR_INVALID_ARG;
+  if (!aligned(dy, dy_type == E4B_F32 ? 4 : 2) || !aligned(dr, 2) || !aligned(r, 2) || !aligned(weight, 2) ||
+      !aligned(rstd, 4) || !aligned(dx, 2))
+    return E4B_ERR_INVALID_ARG;
+  const size_t need = e4b_rmsnorm_backward_workspace_bytes(T, H);
+  if (ws_bytes < need) return E4B_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(T) * H;
+  const Range in[5] = {range_of(dy, n * (dy_type == E4B_F32 ? 4 : 2)), range_of(dr, 2 * n), range_of(r, 2 * n),
+                       range_of(weight, 2 * static_cast<size_t>(H)), range_of(rstd, 4 * static_cast<size_t>(T))};
+  const Range odx = range_of(dx, 2 * n), odw = range_of(dweight, 4 * static_cast<size_t>(H)), w = range_of(ws, need);
+  for (int j = 0; j < 5; ++j)
+    if ((j < 3 ? !same_or_apart(odx, in[j]) : overlap(odx, in[j])) || overlap(odw, in[j]) || overlap(w, in[j]))
+      return E4B_ERR_INVALID_ARG;
+  if (overlap(odx, odw) || overlap(odx, w) || overlap(odw, w)) return E4B_ERR_INVALID_ARG;
+  const NormBackwardLaunch p{dy, dy_type == E4B_F32 ? 1 : 0, dr, r, weight, rstd, T, H, 1.0 / H, dx, dweight,
+                             static_cast<float*>(ws)};
+  return launch_rmsnorm_backward(p, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
+}
+
+static const int32_t kMaxGradTensors = 65536;
+
+size_t e4b_clip_grad_norm_workspace_bytes(int32_t tensors) {
+  if (tensors < 0 || tensors > kMaxGradTensors) return 0;
+  return align_up(grad_norm_partials(tensors) * sizeof(double));
+}
+
+// Whether every out lies apart from every other out and from every grad but its own.
+static e4b_status check_grads(const e4b_grad* g, int32_t tensors, const Range& norm, const Range& ws) {
+  struct Span {
+    Range r;
+    int32_t owner;
+  };
+  Span* outs = new (std::nothrow) Span[tensors > 0 ? tensors : 1];
+  if (!outs) return E4B_ERR_INVALID_ARG;
+  e4b_status st = E4B_OK;
+  int32_t n = 0;
+  auto bytes = [&](int32_t i) { return static_cast<size_t>(g[i].n) * (g[i].dtype == E4B_F32 ? 4 : 2); };
+  for (int32_t i = 0; i < tensors; ++i)
+    if (g[i].n > 0) outs[n++] = {range_of(g[i].out, bytes(i)), i};
+  auto before = [](const Span& a, const Span& b) { return a.r.lo < b.r.lo; };
+  if (!std::is_sorted(outs, outs + n, before)) std::sort(outs, outs + n, before);
+  for (int32_t i = 1; i < n; ++i)
+    if (outs[i].r.lo < outs[i - 1].r.hi) st = E4B_ERR_INVALID_ARG;
+  // the outs are now in order and apart: a grad can only overlap those around it
+  auto clash = [&](const Range& r, int32_t own) {
+    const Span key{r, 0};
+    const Span* it = std::upper_bound(outs, outs + n, key, before);
+    for (const Span* s = it == outs ? it : it - 1; s < outs + n && s->r.lo < r.hi; ++s)
+      if (overlap(s->r, r) && !(s->owner == own && s->r.lo == r.lo)) return true;
+    return false;
+  };
+  for (int32_t i = 0; i < tensors && st == E4B_OK; ++i)
+    if (g[i].n > 0) {
+      const Range r = range_of(g[i].grad, bytes(i));
+      if (clash(r, i) || overlap(r, norm) || overlap(r, ws)) st = E4B_ERR_INVALID_ARG;
+    }
+  if (st == E4B_OK && (clash(norm, -1) || clash(ws, -1) || overlap(norm, ws))) st = E4B_ERR_INVALID_ARG;
+  delete[] outs;
+  return st;
+}
+
+e4b_status e4b_clip_grad_norm(const e4b_grad* grads, int32_t tensors, double max_norm, float* total_norm, void* ws,
+                              size_t ws_bytes, e4b_stream stream) {
+  if (tensors < 0 || tensors > kMaxGradTensors || (tensors > 0 && !grads) || !(max_norm >= 0.0))
+    return E4B_ERR_INVALID_ARG;
+  if (!total_norm || !aligned(total_norm, 4) || !ws || !aligned(ws, kAlign)) return E4B_ERR_INVALID_ARG;
+  const size_t need = e4b_clip_grad_norm_workspace_bytes(tensors);
+  if (ws_bytes < need) return E4B_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < tensors; ++i) {
+    const e4b_grad& g = grads[i];
+    if (g.dtype != E4B_F32 && g.dtype != E4B_BF16 && g.dtype != E4B_F16) return E4B_ERR_UNSUPPORTED;
+    const size_t size = g.dtype == E4B_F32 ? 4 : 2;
+    if (g.n < 0 || g.n > (int64_t(1) << 40)) return E4B_ERR_INVALID_ARG;
+    if (g.n > 0 && (!g.grad || !g.out || !aligned(g.grad, size) || !aligned(g.out, size))) return E4B_ERR_INVALID_ARG;
+  }
+  const e4b_status v = check_grads(grads, tensors, range_of(total_norm, 4), range_of(ws, need));
+  if (v != E4B_OK) return v;
+  return launch_clip_grads(grads, tensors, max_norm, total_norm, static_cast<double*>(ws),
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? E4B_OK
+             : E4B_ERR_CUDA;
 }
 
 e4b_status e4b_device_status(void* ws, e4b_stream stream) {

@@ -1,0 +1,311 @@
+// Global gradient norm over many tensors, and clipping.
+//
+//   norm = sqrt(sum over all tensors of sum g^2),
+//   c    = min(1, max_norm / (norm + 1e-6)),   out = g * c.
+//
+// Two launches for any number of tensors up to kMaxTable (their table travels
+// as a kernel argument, so nothing is copied to the device and a captured
+// graph holds it): the first leaves one fp64 partial sum per block, the second
+// adds those in every block, in the same order, and scales.  No atomics and no
+// counters: the norm has the same bits for the same tensors, and the workspace
+// needs no clearing.  Squares are formed and summed in fp64, so values whose
+// square leaves the fp32 range still count (a gradient of 1e25, or of 1e-30).
+//
+// Both passes are bound by HBM.  Work is dealt in chunks of 16 KB: four 16-byte
+// loads per thread, eight blocks per SM.  The second pass walks the chunks from
+// the last to the first, so that what the first pass read last is still in L2.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "e4b_device.cuh"
+#include "e4b_internal.h"
+
+namespace e4b {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kThreads = 256;
+constexpr int kVecPerThread = 4;
+constexpr int kChunkVecs = kThreads * kVecPerThread;   // 16-byte words per chunk
+constexpr int kBlocksPerSm = 8;
+
+// One tensor of the table.  Its 16-byte words start at the boundary at or
+// below the first element; `skip` elements of the first word are not its own.
+struct ClipEntry {
+  const void* in;
+  void* out;
+  int64_t n;
+  int32_t chunk0;       // first chunk of this tensor among the launch's chunks
+  int16_t type;
+  int8_t skip;
+  int8_t words;         // 1: `in` and `out` have the same offset from a 16-byte boundary
+};
+
+template <int N>
+struct ClipTable {
+  int32_t tensors, chunks;
+  ClipEntry e[N];
+};
+
+__device__ __forceinline__ int type_bytes(int type) { return type == E4B_F32 ? 4 : 2; }
+
+template <int N>
+__device__ __forceinline__ int tensor_of(const ClipTable<N>& t, int chunk) {
+  int lo = 0, hi = t.tensors;             // last tensor with chunk0 <= chunk
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.e[mid].chunk0 <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The elements of one 16-byte word as fp32.
+__device__ __forceinline__ int word_values(const uint4& v, int type, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (type == E4B_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+    return 4;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == E4B_BF16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
+  return 8;
+}
+
+__device__ __forceinline__ uint32_t two_halves(float lo, float hi, int type) {
+  if (type == E4B_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float load_one(const void* p, int64_t i, int type) {
+  if (type == E4B_F32) return static_cast<const float*>(p)[i];
+  if (type == E4B_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+__device__ __forceinline__ void store_one(void* p, int64_t i, int type, float v) {
+  if (type == E4B_F32) static_cast<float*>(p)[i] = v;
+  else if (type == E4B_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = red[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) t += red[w];
+  return t;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ ClipTable<N> t,
+                                                             double* __restrict__ partial) {
+  __shared__ double red[kThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  double sum = 0.0;
+  const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * blockIdx.x / gridDim.x);
+  const int c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
+  int ti = tensor_of(t, c0);
+  for (int c = c0; c < c1; ++c) {
+    while (ti + 1 < t.tensors && t.e[ti + 1].chunk0 <= c) ++ti;
+    const ClipEntry& e = t.e[ti];
+    const int type = e.type, per = 16 / type_bytes(type);
+    const uint8_t* base = static_cast<const uint8_t*>(e.in) - e.skip * type_bytes(type);
+    const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * kChunkVecs + threadIdx.x;
+    const int64_t last = e.n + e.skip;     // elements counted from the first word's start
+    uint4 v[kVecPerThread];
+#pragma unroll
+    for (int i = 0; i < kVecPerThread; ++i) {
+      const int64_t at = (w0 + i * kThreads) * per;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (at >= e.skip && at + per <= last) v[i] = *reinterpret_cast<const uint4*>(base + (w0 + i * kThreads) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kVecPerThread; ++i) {
+      const int64_t at = (w0 + i * kThreads) * per;
+      if (at >= e.skip && at + per <= last) {
+        float f[8];
+        const int m = word_values(v[i], type, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < m) sum = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), sum);
+      } else if (at < last) {              // the first or last word, not wholly the tensor's
+        for (int j = 0; j < per; ++j)
+          if (at + j >= e.skip && at + j < last) {
+            const double g = load_one(e.in, at + j - e.skip, type);
+            sum = fma(g, g, sum);
+          }
+      }
+    }
+  }
+  sum = block_sum(sum, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+// max_norm is +infinity where only the norm is wanted.
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipTable<N> t,
+                                                              const double* __restrict__ partial, int partials,
+                                                              double max_norm, float* __restrict__ total_norm) {
+  __shared__ double red[kThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
+  const double norm = sqrt(block_sum(sum, red));
+  if (total_norm && blockIdx.x == 0 && threadIdx.x == 0) *total_norm = static_cast<float>(norm);
+  const double ratio = max_norm / (norm + 1e-6);
+  const float coef = isinf(max_norm) || ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);   // a NaN norm gives NaN
+  const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * blockIdx.x / gridDim.x);
+  const int c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
+  if (c0 == c1) return;
+  int ti = tensor_of(t, c1 - 1);
+  for (int c = c1 - 1; c >= c0; --c) {
+    while (t.e[ti].chunk0 > c) --ti;
+    const ClipEntry& e = t.e[ti];
+    if (e.in == e.out && coef == 1.0f) continue;          // in place and unclipped: already there
+    const int type = e.type, size = type_bytes(type), per = 16 / size;
+    const uint8_t* base = static_cast<const uint8_t*>(e.in) - e.skip * size;
+    uint8_t* obase = static_cast<uint8_t*>(e.out) - e.skip * size;
+    const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * kChunkVecs + threadIdx.x;
+    const int64_t last = e.n + e.skip;
+    uint4 v[kVecPerThread];
+#pragma unroll
+    for (int i = 0; i < kVecPerThread; ++i) {
+      const int64_t at = (w0 + i * kThreads) * per;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (at >= e.skip && at + per <= last) v[i] = *reinterpret_cast<const uint4*>(base + (w0 + i * kThreads) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kVecPerThread; ++i) {
+      const int64_t at = (w0 + i * kThreads) * per;
+      if (at >= e.skip && at + per <= last) {
+        float f[8];
+        word_values(v[i], type, f);
+        if (e.words) {
+          uint4 o;
+          if (type == E4B_F32)
+            o = make_uint4(__float_as_uint(f[0] * coef), __float_as_uint(f[1] * coef), __float_as_uint(f[2] * coef),
+                           __float_as_uint(f[3] * coef));
+          else
+            o = make_uint4(two_halves(f[0] * coef, f[1] * coef, type), two_halves(f[2] * coef, f[3] * coef, type),
+                           two_halves(f[4] * coef, f[5] * coef, type), two_halves(f[6] * coef, f[7] * coef, type));
+          __stcs(reinterpret_cast<uint4*>(obase + (w0 + i * kThreads) * 16), o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < per) store_one(e.out, at + j - e.skip, type, f[j] * coef);
+        }
+      } else if (at < last) {
+        for (int j = 0; j < per; ++j)
+          if (at + j >= e.skip && at + j < last) {
+            const int64_t k = at + j - e.skip;
+            store_one(e.out, k, type, load_one(e.in, k, type) * coef);
+          }
+      }
+    }
+  }
+}
+
+template <int N>
+void fill_table(ClipTable<N>& t, const e4b_grad* g, int count) {
+  t.tensors = count;
+  int64_t chunk = 0;
+  for (int i = 0; i < count; ++i) {
+    ClipEntry& e = t.e[i];
+    const int size = g[i].dtype == E4B_F32 ? 4 : 2;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(g[i].grad);
+    e.in = g[i].grad;
+    e.out = g[i].out;
+    e.n = g[i].n;
+    e.type = static_cast<int16_t>(g[i].dtype);
+    e.skip = static_cast<int8_t>((a % 16) / size);
+    e.words = reinterpret_cast<uintptr_t>(g[i].out) % 16 == a % 16;
+    e.chunk0 = static_cast<int32_t>(chunk);
+    if (e.n > 0) chunk += ((e.n + e.skip) * size + kChunkVecs * 16 - 1) / (kChunkVecs * 16);
+  }
+  t.chunks = static_cast<int32_t>(chunk);
+}
+
+int blocks_for(int chunks) {
+  const int cap = device_sm_count() * kBlocksPerSm;
+  return chunks < cap ? (chunks > 0 ? chunks : 1) : cap;
+}
+
+template <int N>
+cudaError_t run_norm(const e4b_grad* g, int count, double* partial, int* blocks, cudaStream_t s) {
+  ClipTable<N> t;
+  fill_table(t, g, count);
+  *blocks = blocks_for(t.chunks);
+  return launch_pdl(grad_norm_kernel<N>, dim3(*blocks), dim3(kThreads), 0, s, t, partial);
+}
+
+template <int N>
+cudaError_t run_scale(const e4b_grad* g, int count, const double* partial, int partials, double max_norm,
+                      float* total_norm, cudaStream_t s) {
+  ClipTable<N> t;
+  fill_table(t, g, count);
+  return launch_pdl(grad_scale_kernel<N>, dim3(blocks_for(t.chunks)), dim3(kThreads), 0, s, t, partial, partials,
+                    max_norm, total_norm);
+}
+
+constexpr int kSmall = 64, kMedium = 256, kMaxTable = 960;   // 2, 8 and 30 KB of kernel arguments
+
+}  // namespace
+
+size_t grad_norm_partials(int32_t tensors) {
+  const size_t launches = tensors > 0 ? (static_cast<size_t>(tensors) + kMaxTable - 1) / kMaxTable : 1;
+  return launches * device_sm_count() * kBlocksPerSm;
+}
+
+cudaError_t launch_clip_grads(const e4b_grad* g, int32_t tensors, double max_norm, float* total_norm, double* partial,
+                              cudaStream_t s) {
+  int partials = 0, i = 0;
+  do {
+    const int n = tensors - i < kMaxTable ? tensors - i : kMaxTable;
+    int blocks = 0;
+    const cudaError_t e = n <= kSmall    ? run_norm<kSmall>(g + i, n, partial + partials, &blocks, s)
+                          : n <= kMedium ? run_norm<kMedium>(g + i, n, partial + partials, &blocks, s)
+                                         : run_norm<kMaxTable>(g + i, n, partial + partials, &blocks, s);
+    if (e != cudaSuccess) return e;
+    partials += blocks;
+    i += n;
+  } while (i < tensors);
+  bool in_place = true;
+  for (int32_t k = 0; k < tensors; ++k) in_place = in_place && (g[k].n == 0 || g[k].grad == g[k].out);
+  // only the norm is wanted and nothing moves: one block writes it
+  if (std::isinf(max_norm) && in_place) return run_scale<kSmall>(g, 0, partial, partials, max_norm, total_norm, s);
+  i = 0;
+  do {
+    const int n = tensors - i < kMaxTable ? tensors - i : kMaxTable;
+    float* out = i == 0 ? total_norm : nullptr;
+    const cudaError_t e = n <= kSmall    ? run_scale<kSmall>(g + i, n, partial, partials, max_norm, out, s)
+                          : n <= kMedium ? run_scale<kMedium>(g + i, n, partial, partials, max_norm, out, s)
+                                         : run_scale<kMaxTable>(g + i, n, partial, partials, max_norm, out, s);
+    if (e != cudaSuccess) return e;
+    i += n;
+  } while (i < tensors);
+  return cudaSuccess;
+}
+
+}  // namespace e4b

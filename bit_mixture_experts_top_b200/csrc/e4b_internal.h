@@ -164,6 +164,44 @@ struct BackwardLaunch {
 };
 e4b_status launch_moe_backward(const BackwardLaunch& b, cudaStream_t s);
 
+// RMS norm of [T, H] rows (T >= 1) with the residual's addition; q_format E4B_Q8_NONE, E4B_Q8_ROW or E4B_Q8_MX.
+struct NormLaunch {
+  const uint16_t *x, *residual, *weight;   // residual may be null
+  int32_t T, H;
+  double inv_h, eps;
+  int32_t q_format;
+  uint16_t *r_out, *y;                     // each may be null
+  uint8_t* q;
+  void* q_scales;
+  float* rstd;                             // may be null
+};
+cudaError_t launch_rmsnorm(const NormLaunch& p, cudaStream_t s);
+
+struct NormBackwardLaunch {
+  const void* dy;                          // fp32 (dy_f32) or bf16
+  int32_t dy_f32;
+  const uint16_t *dr, *r, *weight;         // dr may be null
+  const float* rstd;
+  int32_t T, H;
+  double inv_h;
+  uint16_t* dx;
+  float* dweight;
+  float* partial;                          // [norm_backward_blocks(T), H]
+};
+int norm_backward_blocks(int32_t T);
+cudaError_t launch_rmsnorm_backward(const NormBackwardLaunch& p, cudaStream_t s);
+
+// out[n] = sum over rows of in[., n] (fp32, fixed order).
+cudaError_t launch_column_sum(const float* in, int rows, int N, float* out, cudaStream_t s);
+// The same of bf16 rows (N even, 4-byte aligned); partial: [column_sum_bf16_blocks(rows), N] fp32, 8-byte aligned.
+int column_sum_bf16_blocks(int rows);
+cudaError_t launch_column_sum_bf16(const uint16_t* in, int rows, int N, float* partial, float* out, cudaStream_t s);
+
+// Gradient norm and clipping; partial holds grad_norm_partials(tensors) doubles.
+size_t grad_norm_partials(int32_t tensors);
+cudaError_t launch_clip_grads(const e4b_grad* g, int32_t tensors, double max_norm, float* total_norm, double* partial,
+                              cudaStream_t s);
+
 // 2-D tiled tensor map (inner dim contiguous, `row_bytes` apart) through the
 // driver entry point; false when the driver refuses the description.
 bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,

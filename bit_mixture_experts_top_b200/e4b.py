@@ -26,6 +26,9 @@ E4B_STAGE_ROUTE, E4B_STAGE_GATHER, E4B_STAGE_GATE_UP, E4B_STAGE_DOWN, E4B_STAGE_
  E4B_WS_Y) = range(7)
 FORMATS = {"nf4": E4B_NF4, "mxfp4": E4B_MXFP4, "nf4_dq": E4B_NF4_DQ}
 E4B_WS_GU_ABSMAX, E4B_WS_DN_ABSMAX = 7, 8
+E4B_F32, E4B_BF16, E4B_F16 = range(3)
+E4B_Q8_NONE, E4B_Q8_ROW, E4B_Q8_MX = range(3)
+DTYPES = {torch.float32: E4B_F32, torch.bfloat16: E4B_BF16, torch.float16: E4B_F16}
 
 
 class E4BError(RuntimeError):
@@ -69,8 +72,34 @@ def make_nf4_dq(codes, absmax2, offset, table):
     return q
 
 
+class Grad(ctypes.Structure):
+    """e4b_grad: one gradient tensor of e4b_clip_grad_norm."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def make_grads(grads, out=None):
+    """The e4b_grad array of contiguous gradient tensors and of the tensors their clipped values go to (out None:
+    clipped in place); the tensors are kept alive with the array."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError("e4b: one out per gradient tensor")
+    _need_cuda(*grads, *out)
+    for g, o in zip(grads, out):
+        if g.dtype not in DTYPES or o.dtype != g.dtype or o.numel() != g.numel():
+            raise ValueError("e4b: gradients are fp32, bf16 or fp16, and each out has its gradient's type and size")
+        if not (g.is_contiguous() and o.is_contiguous()):
+            raise ValueError("e4b: gradient tensors must be contiguous")
+    a = (Grad * len(grads))(*[Grad(g.data_ptr(), o.data_ptr(), g.numel(), DTYPES[g.dtype], 0)
+                              for g, o in zip(grads, out)])
+    a.tensors = (grads, out)
+    return a
+
+
 _LIB = None
 _vp, _sz, _i32, _i64, _u32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32
+_f64 = ctypes.c_double
 _SIGS = {
     "e4b_abi_version": ([], _i32),
     "e4b_status_string": ([_i32], ctypes.c_char_p),
@@ -93,6 +122,11 @@ _SIGS = {
                                _vp, _sz, _vp], _i32),
     "e4b_moe_backward": ([ctypes.POINTER(MoeDesc), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                           _vp, _sz, _vp], _i32),
+    "e4b_rmsnorm": ([_vp, _vp, _vp, _i32, _i32, _f64, _i32, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "e4b_rmsnorm_backward_workspace_bytes": ([_i32, _i32], _sz),
+    "e4b_rmsnorm_backward": ([_vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
+    "e4b_clip_grad_norm_workspace_bytes": ([_i32], _sz),
+    "e4b_clip_grad_norm": ([_vp, _i32, _f64, _vp, _vp, _sz, _vp], _i32),
     "e4b_device_status": ([_vp, _vp], _i32),
     "e4b_debug_wait_timeout": ([_u32, _vp, _sz, _vp], _i32),
 }
@@ -250,6 +284,36 @@ def e4b_moe_backward(desc, T, logits, dout, gu_codes, gu_scales, dn_codes, dn_sc
                                   _ptr(dlogits), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel() * ws.element_size(),
                                   _stream(stream)), "e4b_moe_backward")
     return dx, dlogits, dA, dB
+
+
+def e4b_rmsnorm(x, residual, weight, T, H, eps, q_format, r_out, y, q, q_scales, rstd, stream=None):
+    _need_cuda(x, residual, weight, r_out, y, q, q_scales, rstd)
+    _check(lib().e4b_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), T, H, eps, q_format, _ptr(r_out), _ptr(y), _ptr(q),
+                             _ptr(q_scales), _ptr(rstd), _stream(stream)), "e4b_rmsnorm")
+
+
+def e4b_rmsnorm_backward_workspace_bytes(T, H):
+    return lib().e4b_rmsnorm_backward_workspace_bytes(T, H)
+
+
+def e4b_rmsnorm_backward(dy, dy_type, dr, r, weight, rstd, T, H, dx, dweight, ws, stream=None):
+    _need_cuda(dy, dr, r, weight, rstd, dx, dweight, ws)
+    _check(lib().e4b_rmsnorm_backward(_ptr(dy), dy_type, _ptr(dr), _ptr(r), _ptr(weight), _ptr(rstd), T, H, _ptr(dx),
+                                      _ptr(dweight), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "e4b_rmsnorm_backward")
+    return dx, dweight
+
+
+def e4b_clip_grad_norm_workspace_bytes(tensors):
+    return lib().e4b_clip_grad_norm_workspace_bytes(tensors)
+
+
+def e4b_clip_grad_norm(grads, max_norm, total_norm, ws, stream=None):
+    """grads: the array of :func:`make_grads`."""
+    _need_cuda(total_norm, ws)
+    _check(lib().e4b_clip_grad_norm(ctypes.cast(grads, ctypes.c_void_p), len(grads), max_norm, _ptr(total_norm),
+                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "e4b_clip_grad_norm")
+    return total_norm
 
 
 def e4b_device_status(ws, stream=None):

@@ -341,6 +341,102 @@ e4b_status e4b_moe_backward(const e4b_moe_desc* d, int32_t T, const uint16_t* lo
                             const uint16_t* lora_A, const uint16_t* lora_B, float* dx, float* dlogits,
                             float* dA, float* dB, void* ws, size_t ws_bytes, e4b_stream stream);
 
+/*
+ * The dense operators of a block around the routed layer: the norm that makes
+ * the layer's input, the feed-forward block of a shared expert that runs next
+ * to the routed ones, and the clipping of the gradients that the backward
+ * calls leave.  [PKG] limits list gives the experts' epilogue that the shared
+ * expert has too; the norm and the clipping are not described by the pages and
+ * are this library's own definitions, stated with each call.
+ */
+
+/* Element types of the arguments that may have several. */
+enum { E4B_F32 = 0, E4B_BF16 = 1, E4B_F16 = 2 };
+
+/* Forms of the norm's 8-bit output (e4m3 codes).
+ * E4B_Q8_ROW: one fp32 scale per row, max(fl32(max|y| / 448), 2^-126);
+ *             q = e4m3(fl32(y / scale)).
+ * E4B_Q8_MX : one E8M0 byte per 32 values (2^(byte - 127), as in the MXFP4
+ *             stacks), with the smallest exponent for which max|y| <= 448 * 2^e
+ *             (not below byte 0); q = e4m3(y * 2^-e).  H a multiple of 32.
+ * A row (a 32-value block) that holds an infinity or a NaN gets a NaN scale
+ * (byte 255) and codes 0x7F. */
+enum { E4B_Q8_NONE = 0, E4B_Q8_ROW = 1, E4B_Q8_MX = 2 };
+
+/*
+ * Root-mean-square norm with the residual's addition.  Per row of H values:
+ *   r = bf16(x + residual)  (r = x when residual is NULL),
+ *   rstd = fl32(1 / sqrt(mean(r^2) + eps)), mean, root and quotient in fp64,
+ *   y = fl32(fl32(r * rstd) * weight), written as bf16 and/or as e4m3.
+ *   x        : [T, H] bf16                          (device, read)
+ *   residual : [T, H] bf16 or NULL                  (device, read)
+ *   weight   : [H] bf16                             (device, read)
+ *   eps      : >= 0, finite
+ *   q_format : E4B_Q8_NONE, E4B_Q8_ROW or E4B_Q8_MX
+ *   r_out    : [T, H] bf16 or NULL, the new stream  (device, written; needs residual)
+ *   y        : [T, H] bf16 or NULL                  (device, written)
+ *   q        : [T, H] e4m3 bytes; q_scales: [T] fp32 (row) or [T, H/32] bytes
+ *              (MX); both NULL with E4B_Q8_NONE     (device, written)
+ *   rstd     : [T] fp32 or NULL                     (device, written) for the backward
+ * One of y and q is required.  r_out or y may be the same buffer as x or
+ * residual (in place); any other overlap of an output with another argument
+ * is refused.  Any H >= 1 and element alignment are accepted; rows of a multiple
+ * of eight values on 16-byte aligned buffers take the fast kernel.
+ */
+e4b_status e4b_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
+                       double eps, int32_t q_format, uint16_t* r_out, uint16_t* y, uint8_t* q, void* q_scales,
+                       float* rstd, e4b_stream stream);
+
+/* Workspace bytes of e4b_rmsnorm_backward (0 on bad sizes). */
+size_t e4b_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H);
+
+/*
+ * Gradients of the norm.  With xh = r * rstd and c = mean over H of dy * weight * xh:
+ *   dx = rstd * (dy * weight - xh * c) (+ dr), the gradient of x and of residual alike,
+ *   dweight = sum over rows of dy * xh (the same bits for the same inputs).
+ *   dy      : [T, H], dy_type E4B_F32 (e4b_moe_backward's dx) or E4B_BF16  (device, read)
+ *   dr      : [T, H] bf16, the gradient that reaches r_out directly, or NULL (device, read)
+ *   r, rstd : the forward's stream [T, H] bf16 and [T] fp32              (device, read)
+ *   dx      : [T, H] bf16                                               (device, written)
+ *   dweight : [H] fp32 (zeros when T == 0)                              (device, written)
+ *   ws      : 256-byte aligned, >= e4b_rmsnorm_backward_workspace_bytes(T, H)
+ * dx may be the same buffer as dr, r or a bf16 dy; other overlaps are refused.
+ */
+e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t* dr, const uint16_t* r,
+                                const uint16_t* weight, const float* rstd, int32_t T, int32_t H, uint16_t* dx,
+                                float* dweight, void* ws, size_t ws_bytes, e4b_stream stream);
+
+/* One gradient tensor of e4b_clip_grad_norm, its elements in one contiguous run. */
+typedef struct {
+  const void* grad;        /* n elements, aligned to the element (device, read) */
+  void* out;               /* n elements (device, written); the same pointer as grad clips in place */
+  int64_t n;               /* elements, >= 0 */
+  int32_t dtype;           /* E4B_F32, E4B_BF16 or E4B_F16, of grad and out */
+  int32_t reserved;        /* 0 */
+} e4b_grad;
+
+/* Workspace bytes of e4b_clip_grad_norm (0 when tensors is out of 0..65536). */
+size_t e4b_clip_grad_norm_workspace_bytes(int32_t tensors);
+
+/*
+ * Global gradient norm over many tensors, and clipping:
+ *   norm = sqrt(sum over all tensors of sum g^2)   (squares and sums in fp64),
+ *   c = fl32(min(1, max_norm / (norm + 1e-6))),  out = g * c rounded to the tensor's type.
+ *   grads      : HOST array of `tensors` descriptions (0..65536 of them); it is
+ *                read before the call returns, the tensors after
+ *   max_norm   : >= 0; +infinity leaves every value as it is (with out == grad
+ *                nothing is written but the norm)
+ *   total_norm : [1] fp32 (device, written), the norm before clipping
+ *   ws         : 256-byte aligned, >= e4b_clip_grad_norm_workspace_bytes(tensors)
+ * A norm that is NaN makes every output NaN, an infinite one makes the finite
+ * values 0.  Tensors of any length and alignment may be mixed.  An out that
+ * overlaps another out, or any grad but its own (and that only as the same
+ * pointer), is refused; so the same tensor cannot be listed twice in place.
+ * The norm has the same bits for the same list of tensors.
+ */
+e4b_status e4b_clip_grad_norm(const e4b_grad* grads, int32_t tensors, double max_norm, float* total_norm, void* ws,
+                              size_t ws_bytes, e4b_stream stream);
+
 /* Stages of e4b_moe_forward, in order. */
 enum {
   E4B_STAGE_ROUTE = 0,     /* clears the status word; top-k, histogram, stable permute */

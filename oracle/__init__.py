@@ -28,6 +28,8 @@ Modules:
 * :mod:`oracle.route`  - top-k routing, expert histogram and stable permute.
 * :mod:`oracle.moe`    - the layer forward: grouped gate_up, LoRA delta,
   SwiGLU, grouped down and the weighted combine.
+* :mod:`oracle.dense`  - the dense operators around the layer: RMS norm (with
+  8-bit outputs), gated feed-forward block, gradient clipping, and backwards.
 
 Parity status of every function is listed in :data:`PINS`; a function whose
 result has no independent pin would say "parity unpinned" there.  Every
@@ -42,5 +44,11 @@ PINS = {
     "nf4.nf4_codebook": "pinned: invariants (sorted, c0=-1, c7=0, c15=1, 7 neg / 8 pos) and the defining quantile equation checked through math.erfc",
     "nf4.quantize_nf4": "pinned: exact round trip of codebook values times powers of two; brute-force nearest-level argmin on random values",
     "route.route": "pinned: brute force full sort per token; constant rows for ties; softmax identity",
+    "dense.round_to_e4m3": "pinned: torch float8_e4m3fn casts on fp32 inputs, every value and every midpoint",
+    "dense.rmsnorm": "pinned: torch rms_norm in fp64; rows of one value; homogeneity",
+    "dense.rmsnorm_backward": "pinned: central finite differences of the fp64 forward",
+    "dense.quantize_mx": "pinned: brute-force search of the exponent; values read back within half a step",
+    "dense.ffn_backward": "pinned: central finite differences of the fp64 forward",
+    "dense.clip_grads": "pinned: torch clip_grad_norm_ in fp64",
     "moe.moe_forward": "pinned: per-token dense loop on tiny inputs; E=1,k=1 textbook SwiGLU FFN; token-permutation invariance; LoRA B=0 equals base",
 }
