@@ -2,7 +2,8 @@
 
 Thin owners of device buffers around the C ABI, as :mod:`layer` is for the
 routed layer: :class:`RmsNorm` (the layer's input from the hidden stream, and
-its backward) and :class:`GradClipper` (the gradients that the backward calls
+its backward), :class:`GluFfn` (the shared expert that runs next to the routed
+ones, forward and backward) and :class:`GradClipper` (the gradients that the backward calls
 leave).  Nothing here computes.
 
 Every call runs on the current stream of the tensors' device.  Outputs and
@@ -114,6 +115,73 @@ class RmsNorm:
             ws = torch.empty(e4b.e4b_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
             e4b.e4b_rmsnorm_backward(dy, e4b.DTYPES[dy.dtype], dr, r, self.weight, rstd, T, H, dx, dw, ws)
         return dx, dw
+
+
+class FfnSaved:
+    """What :meth:`GluFfn.forward_train` keeps for one :meth:`GluFfn.backward`: the input and the workspace with the
+    pre-activations and h."""
+
+    def __init__(self, x, ws):
+        self.x, self.ws = x, ws
+
+
+class GluFfn:
+    """Gated feed-forward block with bf16 weights, the shared expert next to the routed ones:
+    out = act(x W_gate^T + b, x W_up^T + b) W_down^T + b (+ add).
+
+    gate_up [2I, H] bf16 (gate rows, then up rows), down [H, I] bf16, gu_bias [2I] / dn_bias [H] fp32 or None;
+    glu = (alpha, limit, beta) selects the clamped GLU instead of SwiGLU.  H and I are multiples of 8."""
+
+    def __init__(self, gate_up, down, gu_bias=None, dn_bias=None, glu=None):
+        if down.dim() != 2:
+            raise ValueError("e4b: down must be [H, I]")
+        self.H, self.I = down.shape
+        self.down = _check(down, "down", (self.H, self.I), torch.bfloat16)
+        self.gate_up = _check(gate_up, "gate_up", (2 * self.I, self.H), torch.bfloat16)
+        self.gu_bias = None if gu_bias is None else _check(gu_bias, "gu_bias", (2 * self.I,), torch.float32)
+        self.dn_bias = None if dn_bias is None else _check(dn_bias, "dn_bias", (self.H,), torch.float32)
+        self.desc = e4b.make_ffn_desc(self.H, self.I, glu)
+        if e4b.e4b_ffn_workspace_bytes(self.desc, 1) == 0:
+            raise ValueError("e4b: unsupported feed-forward shape (H and I are multiples of 8, the GLU limit is "
+                             "positive)")
+
+    def _run(self, call, nbytes, x, add, out):
+        if x.dim() != 2:
+            raise ValueError("e4b: x must be [T, H]")
+        T = x.shape[0]
+        _check(x, "x", (T, self.H), torch.bfloat16)
+        if add is not None:
+            _check(add, "add", (T, self.H), torch.bfloat16)
+        with _On(x, add, out, self.gate_up, self.down, self.gu_bias, self.dn_bias) as dev:
+            out = torch.empty_like(x) if out is None else _check(out, "out", (T, self.H), torch.bfloat16)
+            ws = torch.empty(nbytes(self.desc, T), dtype=torch.uint8, device=dev)
+            call(self.desc, T, x, self.gate_up, self.down, self.gu_bias, self.dn_bias, add, out, ws)
+        return out, ws
+
+    def forward(self, x, add=None, out=None):
+        """out [T, H] bf16; add [T, H] bf16 is added to it (the routed experts' output), and out may be add."""
+        return self._run(e4b.e4b_ffn_forward, e4b.e4b_ffn_workspace_bytes, x, add, out)[0]
+
+    def forward_train(self, x, add=None, out=None):
+        """(out, saved): the forward, and what :meth:`backward` needs of it."""
+        out, ws = self._run(e4b.e4b_ffn_forward_train, e4b.e4b_ffn_train_workspace_bytes, x, add, out)
+        return out, FfnSaved(x, ws)
+
+    def backward(self, saved, dout, weights=True):
+        """(dx, d_gate_up, d_down, d_gu_bias, d_dn_bias) of sum(dout * out): bf16, the biases' fp32 (None without them).
+        The gradient of add is dout.  weights False: the weights are frozen and only dx is computed, the others None."""
+        T = saved.x.shape[0]
+        _check(dout, "dout", (T, self.H), torch.bfloat16)
+        with _On(saved.x, saved.ws, dout, self.gate_up) as dev:
+            dx = torch.empty_like(saved.x)
+            dgu = torch.empty_like(self.gate_up) if weights else None
+            ddn = torch.empty_like(self.down) if weights else None
+            dbg = torch.empty((2 * self.I,), dtype=torch.float32, device=dev) \
+                if weights and self.gu_bias is not None else None
+            dbd = torch.empty((self.H,), dtype=torch.float32, device=dev) \
+                if weights and self.dn_bias is not None else None
+            e4b.e4b_ffn_backward(self.desc, T, saved.x, dout, self.gate_up, self.down, dx, dgu, ddn, dbg, dbd, saved.ws)
+        return dx, dgu, ddn, dbg, dbd
 
 
 class GradClipper:

@@ -619,6 +619,228 @@ e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t*
   return launch_rmsnorm_backward(p, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------------- gated feed-forward block
+
+static e4b_status validate_ffn(const e4b_ffn_desc* d, int32_t T) {
+  if (!d || T < 0) return E4B_ERR_INVALID_ARG;
+  if (d->H < 8 || d->H % 8 != 0 || d->I < 8 || d->I % 8 != 0) return E4B_ERR_UNSUPPORTED;
+  if (d->I >= (1 << 29) || d->H >= (1 << 29) || T >= (1 << 30)) return E4B_ERR_UNSUPPORTED;
+  if (d->act != E4B_ACT_SWIGLU && d->act != E4B_ACT_CLAMPED_GLU) return E4B_ERR_UNSUPPORTED;
+  if (d->act == E4B_ACT_CLAMPED_GLU &&
+      (!std::isfinite(d->glu_alpha) || !std::isfinite(d->glu_beta) || !(d->glu_limit > 0.0f)))
+    return E4B_ERR_INVALID_ARG;
+  return E4B_OK;
+}
+
+struct FfnLayout {
+  size_t status, h, forward_total;                 // e4b_ffn_forward
+  size_t g, dG, gu_sums, dn_sums, total;           // and the training pair
+};
+
+static FfnLayout ffn_layout(const e4b_ffn_desc& d, int32_t T) {
+  const size_t t = static_cast<size_t>(T), I = static_cast<size_t>(d.I);
+  FfnLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
+    return at;
+  };
+  L.status = take(kStatusBytes);
+  L.h = take(t * I * 2);
+  L.forward_total = o;
+  L.g = take(t * 2 * I * 4);
+  L.dG = take(t * 2 * I * 2);
+  L.gu_sums = take((t + 31) / 32 * 2 * I * 4);
+  L.dn_sums = take(static_cast<size_t>(column_sum_bf16_blocks(T)) * d.H * 4);
+  L.total = o;
+  return L;
+}
+
+size_t e4b_ffn_workspace_bytes(const e4b_ffn_desc* d, int32_t T) {
+  return validate_ffn(d, T) == E4B_OK ? ffn_layout(*d, T).forward_total : 0;
+}
+
+size_t e4b_ffn_train_workspace_bytes(const e4b_ffn_desc* d, int32_t T) {
+  return validate_ffn(d, T) == E4B_OK ? ffn_layout(*d, T).total : 0;
+}
+
+static e4b_status run_ffn(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* w_gu,
+                          const uint16_t* w_dn, const float* gu_bias, const float* dn_bias, const uint16_t* add,
+                          uint16_t* out, void* ws, size_t ws_bytes, e4b_stream stream, bool train) {
+  const e4b_status v = validate_ffn(d, T);
+  if (v != E4B_OK) return v;
+  if (!ws || !aligned(ws, kAlign)) return E4B_ERR_INVALID_ARG;
+  const FfnLayout L = ffn_layout(*d, T);
+  const size_t need = train ? L.total : L.forward_total;
+  if (ws_bytes < need) return E4B_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return cudaMemsetAsync(ws, 0, kStatusBytes, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
+  if (!x || !w_gu || !w_dn || !out) return E4B_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w_gu, 16) || !aligned(w_dn, 16) || !aligned(add, 16) || !aligned(out, 16) ||
+      !aligned(gu_bias, 4) || !aligned(dn_bias, 4))
+    return E4B_ERR_INVALID_ARG;
+  const size_t H = d->H, I = d->I, rows = static_cast<size_t>(T) * H * 2;
+  const Range o = range_of(out, rows), w = range_of(ws, need);
+  const Range in[5] = {range_of(x, rows), range_of(w_gu, 4 * I * H), range_of(w_dn, 2 * I * H),
+                       range_of(gu_bias, 8 * I), range_of(dn_bias, 4 * H)};
+  for (const Range& r : in)
+    if (overlap(o, r) || overlap(w, r)) return E4B_ERR_INVALID_ARG;
+  if (!same_or_apart(o, range_of(add, rows)) || overlap(w, range_of(add, rows)) || overlap(o, w))
+    return E4B_ERR_INVALID_ARG;
+  uint16_t* h = at<uint16_t>(ws, L.h);
+  float* g = train ? at<float>(ws, L.g) : nullptr;
+  int32_t* status = at<int32_t>(ws, L.status);
+  if (T <= kDecodeTokens) {
+    const Epilogue ep{nullptr, d->act, d->glu_alpha, d->glu_limit, d->glu_beta};
+    const DenseDecodeLaunch gu{T, d->I, d->H, x, w_gu, gu_bias, nullptr, h, g, ep, status};
+    const DenseDecodeLaunch dn{T, d->H, d->I, h, w_dn, dn_bias, add, out, nullptr, ep, status};
+    if (launch_dense_decode(gu, true, s) != cudaSuccess || launch_dense_decode(dn, false, s) != cudaSuccess)
+      return E4B_ERR_CUDA;
+    return E4B_OK;
+  }
+  DenseGemmLaunch gu = {};
+  gu.epi = kEpiGateUp;
+  gu.M = T;
+  gu.N = d->I;
+  gu.K = d->H;
+  gu.a = x;
+  gu.b = w_gu;
+  gu.act = d->act;
+  gu.alpha = d->glu_alpha;
+  gu.limit = d->glu_limit;
+  gu.beta = d->glu_beta;
+  gu.bias = gu_bias;
+  gu.out = h;
+  gu.g_out = g;
+  gu.status = status;
+  gu.clear_status = 1;
+  const e4b_status st = launch_dense_gemm(gu, s);
+  if (st != E4B_OK) return st;
+  DenseGemmLaunch dn = {};
+  dn.epi = kEpiLinear;
+  dn.M = T;
+  dn.N = d->H;
+  dn.K = d->I;
+  dn.a = h;
+  dn.b = w_dn;
+  dn.bias = dn_bias;
+  dn.add = add;
+  dn.out = out;
+  dn.status = status;
+  return launch_dense_gemm(dn, s);
+}
+
+e4b_status e4b_ffn_forward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* w_gu,
+                           const uint16_t* w_dn, const float* gu_bias, const float* dn_bias, const uint16_t* add,
+                           uint16_t* out, void* ws, size_t ws_bytes, e4b_stream stream) {
+  return run_ffn(d, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, ws_bytes, stream, false);
+}
+
+e4b_status e4b_ffn_forward_train(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* w_gu,
+                                 const uint16_t* w_dn, const float* gu_bias, const float* dn_bias,
+                                 const uint16_t* add, uint16_t* out, void* ws, size_t ws_bytes, e4b_stream stream) {
+  return run_ffn(d, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, ws_bytes, stream, true);
+}
+
+e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* dout,
+                            const uint16_t* w_gu, const uint16_t* w_dn, uint16_t* dx, uint16_t* dw_gu,
+                            uint16_t* dw_dn, float* dgu_bias, float* ddn_bias, void* ws, size_t ws_bytes,
+                            e4b_stream stream) {
+  const e4b_status v = validate_ffn(d, T);
+  if (v != E4B_OK) return v;
+  if (!ws || !aligned(ws, kAlign)) return E4B_ERR_INVALID_ARG;
+  const FfnLayout L = ffn_layout(*d, T);
+  if (ws_bytes < L.total) return E4B_ERR_INVALID_ARG;
+  if (!aligned(dx, 16) || !aligned(dw_gu, 16) || !aligned(dw_dn, 16) || !aligned(dgu_bias, 4) || !aligned(ddn_bias, 4))
+    return E4B_ERR_INVALID_ARG;
+  const size_t H = d->H, I = d->I, rows = static_cast<size_t>(T) * H * 2;
+  const Range outs[5] = {range_of(dx, rows), range_of(dw_gu, 4 * I * H), range_of(dw_dn, 2 * I * H),
+                         range_of(dgu_bias, 8 * I), range_of(ddn_bias, 4 * H)};
+  const Range ins[5] = {range_of(ws, L.total), range_of(x, rows), range_of(dout, rows), range_of(w_gu, 4 * I * H),
+                        range_of(w_dn, 2 * I * H)};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (overlap(outs[i], ins[j])) return E4B_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return E4B_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const bool ok = (!dw_gu || cudaMemsetAsync(dw_gu, 0, 4 * I * H, s) == cudaSuccess) &&
+                    (!dw_dn || cudaMemsetAsync(dw_dn, 0, 2 * I * H, s) == cudaSuccess) &&
+                    (!dgu_bias || cudaMemsetAsync(dgu_bias, 0, 8 * I, s) == cudaSuccess) &&
+                    (!ddn_bias || cudaMemsetAsync(ddn_bias, 0, 4 * H, s) == cudaSuccess);
+    return ok ? E4B_OK : E4B_ERR_CUDA;
+  }
+  if (!x || !dout || !w_gu || !w_dn || !aligned(x, 16) || !aligned(dout, 16) || !aligned(w_gu, 16) ||
+      !aligned(w_dn, 16))
+    return E4B_ERR_INVALID_ARG;
+  uint16_t* dG = at<uint16_t>(ws, L.dG);
+  DenseGemmLaunch base = {};
+  base.act = d->act;
+  base.alpha = d->glu_alpha;
+  base.limit = d->glu_limit;
+  base.beta = d->glu_beta;
+  base.status = at<int32_t>(ws, L.status);
+  e4b_status st = E4B_OK;
+  if (dx || dw_gu || dgu_bias) {                     // dG = act'(G) applied to dout W_dn
+    DenseGemmLaunch g = base;
+    g.epi = kEpiDact;
+    g.M = T;
+    g.N = d->I;
+    g.K = d->H;
+    g.a = dout;
+    g.b = w_dn;
+    g.b_mn = true;
+    g.out = dG;
+    g.g_in = at<float>(ws, L.g);
+    g.colsum = dgu_bias ? at<float>(ws, L.gu_sums) : nullptr;
+    st = launch_dense_gemm(g, s);
+    if (st != E4B_OK) return st;
+  }
+  base.epi = kEpiLinear;
+  if (dx) {                                          // dx = dG W_gu
+    DenseGemmLaunch g = base;
+    g.M = T;
+    g.N = d->H;
+    g.K = 2 * d->I;
+    g.a = dG;
+    g.b = w_gu;
+    g.b_mn = true;
+    g.out = dx;
+    st = launch_dense_gemm(g, s);
+    if (st != E4B_OK) return st;
+  }
+  base.a_mn = base.b_mn = true;                      // both contract the tokens
+  base.K = T;
+  if (dw_gu) {                                       // dG^T x
+    DenseGemmLaunch g = base;
+    g.M = 2 * d->I;
+    g.N = d->H;
+    g.a = dG;
+    g.b = x;
+    g.out = dw_gu;
+    st = launch_dense_gemm(g, s);
+    if (st != E4B_OK) return st;
+  }
+  if (dw_dn) {                                       // dout^T h
+    DenseGemmLaunch g = base;
+    g.M = d->H;
+    g.N = d->I;
+    g.a = dout;
+    g.b = at<uint16_t>(ws, L.h);
+    g.out = dw_dn;
+    st = launch_dense_gemm(g, s);
+    if (st != E4B_OK) return st;
+  }
+  if (dgu_bias && launch_column_sum(at<float>(ws, L.gu_sums), (T + 31) / 32, 2 * d->I, dgu_bias, s) != cudaSuccess)
+    return E4B_ERR_CUDA;
+  if (ddn_bias && launch_column_sum_bf16(dout, T, d->H, at<float>(ws, L.dn_sums), ddn_bias, s) != cudaSuccess)
+    return E4B_ERR_CUDA;
+  return E4B_OK;
+}
+
 static const int32_t kMaxGradTensors = 65536;
 
 size_t e4b_clip_grad_norm_workspace_bytes(int32_t tensors) {

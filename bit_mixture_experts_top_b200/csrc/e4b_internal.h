@@ -202,6 +202,43 @@ size_t grad_norm_partials(int32_t tensors);
 cudaError_t launch_clip_grads(const e4b_grad* g, int32_t tensors, double max_norm, float* total_norm, double* partial,
                               cudaStream_t s);
 
+// Dense bf16 products on tcgen05: D[M, N] = sum over k of A[m, k] B[n, k] with an epilogue.  An operand is
+// K-contiguous ([rows, K]) or, with a_mn / b_mn, row-contiguous ([K, rows]); every extent is a multiple of 8
+// where it is the contiguous one.  Pointers 16-byte aligned.
+enum { kEpiGateUp = 0, kEpiLinear = 1, kEpiDact = 2 };
+struct DenseGemmLaunch {
+  int32_t epi;
+  int32_t M, N, K;            // gate_up: N = I, B = [2I, K]; dact: N = I
+  bool a_mn, b_mn;            // dact: B is [K, I]
+  const uint16_t *a, *b;
+  int32_t act;
+  float alpha, limit, beta;
+  const float* bias;          // gate_up [2I], linear [N], or null
+  const uint16_t* add;        // linear: [M, N] or null
+  uint16_t* out;              // gate_up: h [M, I]; linear: [M, N]; dact: dG [M, 2I]
+  float* g_out;               // gate_up: G [M, 2I] or null
+  const float* g_in;          // dact: G [M, 2I]
+  float* colsum;              // dact: [ceil(M / 32), 2I] or null
+  int32_t* status;
+  int32_t clear_status;
+};
+e4b_status launch_dense_gemm(const DenseGemmLaunch& g, cudaStream_t s);
+
+// The same products for at most kDecodeTokens tokens, bound by the weight stream.  The down launch (gate_up false)
+// has to follow the gate_up launch that writes its x directly on the stream.
+constexpr int kDecodeTokens = 16;
+struct DenseDecodeLaunch {
+  int32_t T, N, K;            // gate_up: N = I, w = [2I, K]; down: w = [N, K]
+  const uint16_t *x, *w;
+  const float* bias;
+  const uint16_t* add;
+  uint16_t* out;
+  float* g_out;
+  Epilogue ep;
+  int32_t* status;            // cleared by the gate_up launch
+};
+cudaError_t launch_dense_decode(const DenseDecodeLaunch& p, bool gate_up, cudaStream_t s);
+
 // 2-D tiled tensor map (inner dim contiguous, `row_bytes` apart) through the
 // driver entry point; false when the driver refuses the description.
 bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,

@@ -58,6 +58,17 @@ def make_desc(E, H, I, k, fmt, lora_rank=0, lora_scale=0.0, tokens_per_tile=0, g
     return MoeDesc(E, H, I, k, f, lora_rank, lora_scale, E4B_ACT_CLAMPED_GLU, tokens_per_tile, a, lim, b, g)
 
 
+class FfnDesc(ctypes.Structure):
+    """e4b_ffn_desc."""
+    _fields_ = [("H", ctypes.c_int32), ("I", ctypes.c_int32), ("act", ctypes.c_int32), ("glu_alpha", ctypes.c_float),
+                ("glu_limit", ctypes.c_float), ("glu_beta", ctypes.c_float)]
+
+
+def make_ffn_desc(H, I, glu=None):
+    """glu None: SwiGLU; glu = (alpha, limit, beta): the clamped GLU."""
+    return FfnDesc(H, I, E4B_ACT_SWIGLU, 0.0, 0.0, 0.0) if glu is None else FfnDesc(H, I, E4B_ACT_CLAMPED_GLU, *glu)
+
+
 class Nf4DQ(ctypes.Structure):
     """e4b_nf4_dq: a double-quantised absmax (device tensors codes u8, absmax2 f32, offset f32 [1], table f32
     [256]); the tensors are kept alive with the struct."""
@@ -125,6 +136,12 @@ _SIGS = {
     "e4b_rmsnorm": ([_vp, _vp, _vp, _i32, _i32, _f64, _i32, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "e4b_rmsnorm_backward_workspace_bytes": ([_i32, _i32], _sz),
     "e4b_rmsnorm_backward": ([_vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
+    "e4b_ffn_workspace_bytes": ([ctypes.POINTER(FfnDesc), _i32], _sz),
+    "e4b_ffn_train_workspace_bytes": ([ctypes.POINTER(FfnDesc), _i32], _sz),
+    "e4b_ffn_forward": ([ctypes.POINTER(FfnDesc), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "e4b_ffn_forward_train": ([ctypes.POINTER(FfnDesc), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "e4b_ffn_backward": ([ctypes.POINTER(FfnDesc), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                         _i32),
     "e4b_clip_grad_norm_workspace_bytes": ([_i32], _sz),
     "e4b_clip_grad_norm": ([_vp, _i32, _f64, _vp, _vp, _sz, _vp], _i32),
     "e4b_device_status": ([_vp, _vp], _i32),
@@ -302,6 +319,38 @@ def e4b_rmsnorm_backward(dy, dy_type, dr, r, weight, rstd, T, H, dx, dweight, ws
                                       _ptr(dweight), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "e4b_rmsnorm_backward")
     return dx, dweight
+
+
+def e4b_ffn_workspace_bytes(desc, T):
+    return lib().e4b_ffn_workspace_bytes(ctypes.byref(desc), T)
+
+
+def e4b_ffn_train_workspace_bytes(desc, T):
+    return lib().e4b_ffn_train_workspace_bytes(ctypes.byref(desc), T)
+
+
+def e4b_ffn_forward(desc, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, stream=None):
+    _need_cuda(x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws)
+    _check(lib().e4b_ffn_forward(ctypes.byref(desc), T, _ptr(x), _ptr(w_gu), _ptr(w_dn), _ptr(gu_bias), _ptr(dn_bias),
+                                 _ptr(add), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "e4b_ffn_forward")
+    return out
+
+
+def e4b_ffn_forward_train(desc, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, stream=None):
+    _need_cuda(x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws)
+    _check(lib().e4b_ffn_forward_train(ctypes.byref(desc), T, _ptr(x), _ptr(w_gu), _ptr(w_dn), _ptr(gu_bias),
+                                       _ptr(dn_bias), _ptr(add), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
+                                       _stream(stream)), "e4b_ffn_forward_train")
+    return out
+
+
+def e4b_ffn_backward(desc, T, x, dout, w_gu, w_dn, dx, dw_gu, dw_dn, dgu_bias, ddn_bias, ws, stream=None):
+    _need_cuda(x, dout, w_gu, w_dn, dx, dw_gu, dw_dn, dgu_bias, ddn_bias, ws)
+    _check(lib().e4b_ffn_backward(ctypes.byref(desc), T, _ptr(x), _ptr(dout), _ptr(w_gu), _ptr(w_dn), _ptr(dx),
+                                  _ptr(dw_gu), _ptr(dw_dn), _ptr(dgu_bias), _ptr(ddn_bias), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)), "e4b_ffn_backward")
+    return dx, dw_gu, dw_dn, dgu_bias, ddn_bias
 
 
 def e4b_clip_grad_norm_workspace_bytes(tensors):

@@ -406,6 +406,67 @@ e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t*
                                 const uint16_t* weight, const float* rstd, int32_t T, int32_t H, uint16_t* dx,
                                 float* dweight, void* ws, size_t ws_bytes, e4b_stream stream);
 
+/*
+ * Gated feed-forward block with bf16 weights: the shared (dense) expert that
+ * runs next to the routed ones, with their epilogue and layout.
+ *   [g | u] = x W_gu^T + b_gu,  h = act(g, u) rounded to bf16,
+ *   out = h W_dn^T + b_dn + add, rounded to bf16.
+ */
+typedef struct {
+  int32_t H;               /* hidden size, a multiple of 8 */
+  int32_t I;               /* intermediate size, a multiple of 8 */
+  int32_t act;             /* E4B_ACT_SWIGLU or E4B_ACT_CLAMPED_GLU */
+  float glu_alpha;         /* as in e4b_moe_desc */
+  float glu_limit;
+  float glu_beta;
+} e4b_ffn_desc;
+
+/* Workspace bytes of e4b_ffn_forward, and of e4b_ffn_forward_train with
+ * e4b_ffn_backward, at T tokens (0 on a bad desc). */
+size_t e4b_ffn_workspace_bytes(const e4b_ffn_desc* d, int32_t T);
+size_t e4b_ffn_train_workspace_bytes(const e4b_ffn_desc* d, int32_t T);
+
+/*
+ * Forward of the gated feed-forward block; fp32 accumulation and epilogues.
+ *   x       : [T, H] bf16                                     (device, read)
+ *   w_gu    : [2I, H] bf16, gate rows 0..I-1 then up rows     (device, read)
+ *   w_dn    : [H, I] bf16                                     (device, read)
+ *   gu_bias : [2I] fp32 or NULL;  dn_bias : [H] fp32 or NULL  (device, read)
+ *   add     : [T, H] bf16 or NULL: added to the output, e.g. the routed
+ *             experts' output or the residual                 (device, read)
+ *   out     : [T, H] bf16; may be the same buffer as add      (device, written)
+ *   ws      : 256-byte aligned, >= the workspace query; its first bytes hold
+ *             the device status word (e4b_device_status)
+ * bf16 tensors are 16-byte aligned, fp32 ones 4-byte.  Up to 16 tokens run on
+ * the weight-streaming kernel, more on the tcgen05 tiles.
+ */
+e4b_status e4b_ffn_forward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* w_gu,
+                           const uint16_t* w_dn, const float* gu_bias, const float* dn_bias, const uint16_t* add,
+                           uint16_t* out, void* ws, size_t ws_bytes, e4b_stream stream);
+
+/* e4b_ffn_forward that keeps, in its larger workspace, what e4b_ffn_backward
+ * needs: h and the pre-activation [g | u] in fp32. */
+e4b_status e4b_ffn_forward_train(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* w_gu,
+                                 const uint16_t* w_dn, const float* gu_bias, const float* dn_bias,
+                                 const uint16_t* add, uint16_t* out, void* ws, size_t ws_bytes, e4b_stream stream);
+
+/*
+ * Gradients of sum(dout * out) for the forward last run by
+ * e4b_ffn_forward_train on this workspace (same desc, T, x and weights):
+ *   dh = dout W_dn;  dG = act'(G) applied to dh (bf16 operand of what follows);
+ *   dx = dG W_gu;  dw_gu = dG^T x;  dw_dn = dout^T h;
+ *   dgu_bias = column sums of dG (before its rounding), ddn_bias of dout.
+ *   dout     : [T, H] bf16, 16-byte aligned; the gradient of add is dout itself
+ *   dx       : [T, H] bf16;  dw_gu : [2I, H] bf16;  dw_dn : [H, I] bf16
+ *   dgu_bias : [2I] fp32;    ddn_bias : [H] fp32    (device, written)
+ * An output that is NULL is not computed (frozen weights).  With T == 0 the
+ * weight and bias gradients are zeros.  No output may overlap anything else.
+ */
+e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* dout,
+                            const uint16_t* w_gu, const uint16_t* w_dn, uint16_t* dx, uint16_t* dw_gu,
+                            uint16_t* dw_dn, float* dgu_bias, float* ddn_bias, void* ws, size_t ws_bytes,
+                            e4b_stream stream);
+
 /* One gradient tensor of e4b_clip_grad_norm, its elements in one contiguous run. */
 typedef struct {
   const void* grad;        /* n elements, aligned to the element (device, read) */

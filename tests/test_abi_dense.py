@@ -85,16 +85,56 @@ def test_clip_refusals(L):
         assert _clip(L, items[::-1]) == BAD, items
 
 
-def test_grad_struct_matches_the_header(tmp_path):
+def _ffn(L, d, train=False, T=32, x=MB, gu=2 * MB, dn=3 * MB, bg=4 * MB, bd=5 * MB, add=6 * MB, out=7 * MB, ws=8 * MB,
+         n=16 * MB):
+    call = L.e4b_ffn_forward_train if train else L.e4b_ffn_forward
+    return call(ctypes.byref(d), T, x, gu, dn, bg, bd, add, out, ws, n, None)
+
+
+def _ffn_bwd(L, d, T=32, x=MB, dout=2 * MB, gu=3 * MB, dn=4 * MB, dx=5 * MB, dgu=6 * MB, ddn=7 * MB, bg=8 * MB, bd=9 * MB,
+             ws=10 * MB, n=16 * MB):
+    return L.e4b_ffn_backward(ctypes.byref(d), T, x, dout, gu, dn, dx, dgu, ddn, bg, bd, ws, n, None)
+
+
+def test_ffn_refusals(L):
+    d = e4b.make_ffn_desc(64, 128)
+    fw, tr = e4b.e4b_ffn_workspace_bytes(d, 32), e4b.e4b_ffn_train_workspace_bytes(d, 32)
+    assert fw % 256 == 0 and fw >= 32 * 128 * 2 and tr >= fw + 32 * 256 * (4 + 2)
+    for bad in [e4b.make_ffn_desc(60, 128), e4b.make_ffn_desc(64, 100), e4b.make_ffn_desc(0, 128),
+                e4b.make_ffn_desc(64, -8), e4b.make_ffn_desc(64, 128, (1.702, 0.0, 1.0)),
+                e4b.make_ffn_desc(64, 128, (1.702, float("nan"), 1.0)),
+                e4b.make_ffn_desc(64, 128, (float("inf"), 7.0, 1.0)), e4b.FfnDesc(64, 128, 5, 0, 0, 0)]:
+        assert e4b.e4b_ffn_workspace_bytes(bad, 32) == 0 and e4b.e4b_ffn_train_workspace_bytes(bad, 32) == 0
+        assert _ffn(L, bad) in (BAD, UNSUP) and _ffn_bwd(L, bad) in (BAD, UNSUP)
+    assert L.e4b_ffn_forward(None, 32, *[MB] * 8, MB, None) == BAD and e4b.e4b_ffn_workspace_bytes(d, -1) == 0
+    bad = [dict(T=-1), dict(x=None), dict(gu=None), dict(dn=None), dict(out=None), dict(ws=None), dict(ws=8 * MB + 16),
+           dict(x=MB + 8), dict(gu=2 * MB + 8), dict(dn=3 * MB + 8), dict(add=6 * MB + 8), dict(out=7 * MB + 8),
+           dict(bg=4 * MB + 2), dict(bd=5 * MB + 2),
+           dict(out=MB), dict(out=2 * MB), dict(out=3 * MB + 16), dict(out=5 * MB), dict(out=6 * MB + 16), dict(out=8 * MB),
+           dict(x=8 * MB), dict(add=8 * MB)]
+    for kw in bad:
+        assert _ffn(L, d, **kw) == BAD, kw
+        assert _ffn(L, d, train=True, **kw) == BAD, kw
+    assert _ffn(L, d, n=fw - 1) == BAD and _ffn(L, d, train=True, n=tr - 1) == BAD
+    bad = [dict(T=-1), dict(x=None), dict(dout=None), dict(gu=None), dict(dn=None), dict(ws=None), dict(n=tr - 1),
+           dict(x=MB + 8), dict(dout=2 * MB + 8), dict(dx=5 * MB + 8), dict(dgu=6 * MB + 2), dict(ddn=7 * MB + 8),
+           dict(bg=8 * MB + 2), dict(dx=MB), dict(dx=2 * MB), dict(dgu=3 * MB), dict(ddn=6 * MB + 16), dict(bd=8 * MB),
+           dict(dx=10 * MB), dict(bg=10 * MB + 4096)]
+    for kw in bad:
+        assert _ffn_bwd(L, d, **kw) == BAD, kw
+
+
+@pytest.mark.parametrize("cname,py", [("e4b_grad", e4b.Grad), ("e4b_ffn_desc", e4b.FfnDesc)])
+def test_structs_match_the_header(tmp_path, cname, py):
     src = tmp_path / "g.c"
-    fields = [f for f, _ in e4b.Grad._fields_]
+    fields = [f for f, _ in py._fields_]
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "e4b.h"\nint main(void) {\n  printf("%zu", '
-                   "sizeof(e4b_grad));\n" +
-                   "".join(f'  printf(" %zu", offsetof(e4b_grad, {f}));\n' for f in fields) + "  return 0;\n}\n")
+                   f"sizeof({cname}));\n" +
+                   "".join(f'  printf(" %zu", offsetof({cname}, {f}));\n' for f in fields) + "  return 0;\n}\n")
     inc = e4b.HEADER.rsplit("/", 1)[0]
     subprocess.run(["gcc", "-std=c99", "-I", inc, str(src), "-o", str(tmp_path / "g")], check=True)
     got = subprocess.run([str(tmp_path / "g")], check=True, capture_output=True, text=True).stdout.split()
-    assert [int(v) for v in got] == [ctypes.sizeof(e4b.Grad)] + [getattr(e4b.Grad, f).offset for f in fields]
+    assert [int(v) for v in got] == [ctypes.sizeof(py)] + [getattr(py, f).offset for f in fields]
 
 
 def test_classes_refuse_cpu_tensors_and_wrong_shapes():
@@ -106,5 +146,7 @@ def test_classes_refuse_cpu_tensors_and_wrong_shapes():
         block.GradClipper([torch.ones(4)])
     with pytest.raises(ValueError):
         block.GradClipper([])
+    with pytest.raises(ValueError, match="CUDA"):
+        block.GluFfn(torch.ones(16, 8, dtype=torch.bfloat16), torch.ones(8, 8, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="one out per"):
         e4b.make_grads([torch.ones(4)], [])
