@@ -10,6 +10,8 @@ Every call runs on the current stream of the tensors' device.  Outputs and
 workspaces are allocated per call from torch's allocator, so calls on several
 streams, and calls captured into several graphs, share nothing.
 """
+import contextlib
+
 import torch
 
 from . import e4b
@@ -17,9 +19,9 @@ from . import e4b
 
 def _check(t, name, shape, *dtypes):
     """A contiguous CUDA tensor of this shape and one of these types, or ValueError."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise ValueError(f"e4b: {name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"e4b: {name} must be {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)}, "
                          f"got {t.dtype} of {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -27,25 +29,15 @@ def _check(t, name, shape, *dtypes):
     return t
 
 
-class _On:
-    """Makes the tensors' device the current one for a call; all of them must be on it."""
+_HERE = contextlib.nullcontext()
 
-    def __init__(self, *tensors):
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1:
-            raise ValueError(f"e4b: tensors on several devices: {sorted(map(str, devices))}")
-        self.device = devices.pop()
-        self.guard = None if self.device.index == torch.cuda.current_device() else torch.cuda.device(self.device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.device
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _on(index, *tensors):
+    """A context in which device ``index`` is the current one; every tensor has to be on it."""
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"e4b: a tensor on {t.device} in a call on cuda:{index}")
+    return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
 class RmsNorm:
@@ -58,6 +50,7 @@ class RmsNorm:
             raise ValueError("e4b: weight must be [H]")
         self.H, self.eps = weight.numel(), float(eps)
         self.weight = _check(weight, "weight", (self.H,), torch.bfloat16)
+        self.index = weight.get_device()
 
     def _run(self, x, residual, q_format, want_rstd):
         if x.dim() != 2:
@@ -66,16 +59,16 @@ class RmsNorm:
         _check(x, "x", (T, H), torch.bfloat16)
         if residual is not None:
             _check(residual, "residual", (T, H), torch.bfloat16)
-        with _On(x, residual, self.weight) as dev:
+        with _on(self.index, x, residual):
             r = x if residual is None else torch.empty_like(x)
             y = q = scales = None
             if q_format == e4b.E4B_Q8_NONE:
                 y = torch.empty_like(x)
             else:
-                q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
-                scales = torch.empty((T,), dtype=torch.float32, device=dev) if q_format == e4b.E4B_Q8_ROW else \
-                    torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
-            rstd = torch.empty((T,), dtype=torch.float32, device=dev) if want_rstd else None
+                q = x.new_empty((T, H), dtype=torch.float8_e4m3fn)
+                scales = x.new_empty((T,), dtype=torch.float32) if q_format == e4b.E4B_Q8_ROW else \
+                    x.new_empty((T, H // 32), dtype=torch.uint8)
+            rstd = x.new_empty((T,), dtype=torch.float32) if want_rstd else None
             e4b.e4b_rmsnorm(x, residual, self.weight, T, H, self.eps, q_format, r if residual is not None else None, y,
                             q, scales, rstd)
         return y, q, scales, r, rstd
@@ -109,10 +102,10 @@ class RmsNorm:
         _check(dy, "dy", (T, H), torch.float32, torch.bfloat16)
         if dr is not None:
             _check(dr, "dr", (T, H), torch.bfloat16)
-        with _On(dy, r, rstd, dr, self.weight) as dev:
+        with _on(self.index, dy, r, rstd, dr):
             dx = torch.empty_like(r)
-            dw = torch.empty((H,), dtype=torch.float32, device=dev)
-            ws = torch.empty(e4b.e4b_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
+            dw = r.new_empty((H,), dtype=torch.float32)
+            ws = r.new_empty(e4b.e4b_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8)
             e4b.e4b_rmsnorm_backward(dy, e4b.DTYPES[dy.dtype], dr, r, self.weight, rstd, T, H, dx, dw, ws)
         return dx, dw
 
@@ -140,7 +133,9 @@ class GluFfn:
         self.gate_up = _check(gate_up, "gate_up", (2 * self.I, self.H), torch.bfloat16)
         self.gu_bias = None if gu_bias is None else _check(gu_bias, "gu_bias", (2 * self.I,), torch.float32)
         self.dn_bias = None if dn_bias is None else _check(dn_bias, "dn_bias", (self.H,), torch.float32)
-        self.desc = e4b.make_ffn_desc(self.H, self.I, glu)
+        self.index = self.down.get_device()
+        with _on(self.index, self.gate_up, self.gu_bias, self.dn_bias):
+            self.desc = e4b.make_ffn_desc(self.H, self.I, glu)
         if e4b.e4b_ffn_workspace_bytes(self.desc, 1) == 0:
             raise ValueError("e4b: unsupported feed-forward shape (H and I are multiples of 8, the GLU limit is "
                              "positive)")
@@ -152,9 +147,9 @@ class GluFfn:
         _check(x, "x", (T, self.H), torch.bfloat16)
         if add is not None:
             _check(add, "add", (T, self.H), torch.bfloat16)
-        with _On(x, add, out, self.gate_up, self.down, self.gu_bias, self.dn_bias) as dev:
+        with _on(self.index, x, add, out):
             out = torch.empty_like(x) if out is None else _check(out, "out", (T, self.H), torch.bfloat16)
-            ws = torch.empty(nbytes(self.desc, T), dtype=torch.uint8, device=dev)
+            ws = x.new_empty(nbytes(self.desc, T), dtype=torch.uint8)
             call(self.desc, T, x, self.gate_up, self.down, self.gu_bias, self.dn_bias, add, out, ws)
         return out, ws
 
@@ -172,13 +167,13 @@ class GluFfn:
         The gradient of add is dout.  weights False: the weights are frozen and only dx is computed, the others None."""
         T = saved.x.shape[0]
         _check(dout, "dout", (T, self.H), torch.bfloat16)
-        with _On(saved.x, saved.ws, dout, self.gate_up) as dev:
+        with _on(self.index, saved.x, dout):
             dx = torch.empty_like(saved.x)
             dgu = torch.empty_like(self.gate_up) if weights else None
             ddn = torch.empty_like(self.down) if weights else None
-            dbg = torch.empty((2 * self.I,), dtype=torch.float32, device=dev) \
+            dbg = dout.new_empty((2 * self.I,), dtype=torch.float32) \
                 if weights and self.gu_bias is not None else None
-            dbd = torch.empty((self.H,), dtype=torch.float32, device=dev) \
+            dbd = dout.new_empty((self.H,), dtype=torch.float32) \
                 if weights and self.dn_bias is not None else None
             e4b.e4b_ffn_backward(self.desc, T, saved.x, dout, self.gate_up, self.down, dx, dgu, ddn, dbg, dbd, saved.ws)
         return dx, dgu, ddn, dbg, dbd
@@ -192,17 +187,19 @@ class GradClipper:
     def __init__(self, grads, out=None):
         """out: tensors of the same types and sizes that take the clipped values; None clips in place."""
         self.grads = e4b.make_grads(grads, out)
-        everything = [t for ts in self.grads.tensors for t in ts]
-        if not everything:
+        tensors = [t for ts in self.grads.tensors for t in ts]
+        if not tensors:
             raise ValueError("e4b: no gradient tensors")
-        with _On(*everything) as dev:
-            self.device = dev
+        self.index = tensors[0].get_device()
+        with _on(self.index, *tensors):
+            self.ws_bytes = e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads))
 
     def clip(self, max_norm):
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before clipping, a 0-d fp32
         tensor on the device.  max_norm float("inf"): the norm alone."""
-        with _On(self.grads.tensors[0][0]) as dev:
-            norm = torch.empty((), dtype=torch.float32, device=dev)
-            ws = torch.empty(e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads)), dtype=torch.uint8, device=dev)
+        with _on(self.index):
+            first = self.grads.tensors[0][0]
+            norm = first.new_empty((), dtype=torch.float32)
+            ws = first.new_empty(self.ws_bytes, dtype=torch.uint8)
             e4b.e4b_clip_grad_norm(self.grads, float(max_norm), norm, ws)
         return norm

@@ -11,6 +11,10 @@
 // W_dn, dW = dG^T x contracts the tokens), so no transposed copy exists.  TMA
 // brings 128-byte-swizzled boxes either way; only the matrix descriptors differ.
 //
+// Large products run on CTA pairs (CG = 2): one MMA spans both SMs, 256 rows by
+// 256 columns, and each CTA loads its 128 rows of A and half of B, 32 KB per 64
+// of K where a single CTA with the same width loads 48 KB.  No multicast.
+//
 // One persistent CTA per SM.  Warp 0 issues the TMA loads, warp 1 owns tensor
 // memory and issues the MMAs (M = 128 rows, N = BN columns, two accumulators),
 // warps 4-11 run the epilogue of one tile while the next is multiplied.  Every
@@ -35,14 +39,15 @@ constexpr int THREADS = 32 * (WARP_EPI0 + EPI_WARPS);
 constexpr uint64_t kDrainNs = 50000000ull;
 constexpr int kGroupM = 16;              // row tiles that share a sweep over the columns (L2 reuse of both operands)
 
-template <int BN>
+template <int BN, int CG>
 struct Cfg {
   static constexpr int A_BYTES = BM * BK * 2;
-  static constexpr int B_BYTES = BN * BK * 2;
+  static constexpr int B_ROWS = BN / CG;                      // this CTA's share of B
+  static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 196608 / STAGE_BYTES;         // 4, 6 or 8
+  static constexpr int STAGES = 196608 / STAGE_BYTES;         // 4, 6 or 8 (pairs: 6)
   static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // + slack to align the base
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -130,20 +135,22 @@ __device__ __forceinline__ float warp_column_sum16(float (&v)[16], int lane, int
   return v[0] + __shfl_xor_sync(kFull, v[0], 1);
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
+template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
     dense_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const Params p) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, CG>;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 2;
+  uint64_t* s_never = acc_empty + 2;        // a barrier that nothing arrives on
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int32_t* s_abort = reinterpret_cast<int32_t*>(smem + C::OFF_MISC + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;          // rank 0 issues the pair's MMAs
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -152,8 +159,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], EPI_WARPS);
+      mbar_init(&acc_empty[b], CG * EPI_WARPS);
     }
+    mbar_init(s_never, 1);
     *s_abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
@@ -164,47 +172,61 @@ __global__ void __launch_bounds__(THREADS, 1)
   // a wait can only run out seconds after this, so the clearing needs no ordering among the blocks
   if (p.clear_status && blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
   if (warp == WARP_MMA) {
-    tmem_alloc(s_tmem, C::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(s_tmem, C::TMEM_COLS);
+    } else {
+      tmem_alloc(s_tmem, C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();         // the other CTA's barriers and tensor memory are ready too
   tc_fence_after_sync();
   const uint32_t tmem_base = *s_tmem;
   const WaitCtx wctx{s_abort, p.status, p.wait_limit_ns};
   const int total = p.m_tiles * p.n_tiles;
   const int ksteps = (p.K + BK - 1) / BK;
   constexpr int NT = EPI == kEpiGateUp ? BN / 2 : BN;   // output columns (features) per tile
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == WARP_TMA) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, armed = 0, par = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int tile = first; ok && tile < total; tile += step) {
         int mt, nt;
         tile_at(p, tile, mt, nt);
-        const int m0 = mt * BM, n0 = nt * NT;
+        const int m0 = (mt * CG + rank) * BM, n0 = nt * NT;
         for (int ks = 0; ks < ksteps; ++ks) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, wctx, 1101)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
+          const uint32_t bar = CG == 2 ? cluster_addr(&full[stage], 0) : 0;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+            if constexpr (CG == 2) tma_load_2d_pair(dst, map, bar, x, y);
+            else tma_load_2d(dst, map, &full[stage], x, y);
+          };
           uint8_t* a = smem + stage * C::STAGE_BYTES;
           uint8_t* b = a + C::A_BYTES;
           const int k0 = ks * BK;
           if constexpr (A_MN) {
 #pragma unroll
-            for (int i = 0; i < BM / 64; ++i) tma_load_2d(a + i * 8192, &tm_a, &full[stage], m0 + 64 * i, k0);
+            for (int i = 0; i < BM / 64; ++i) load(a + i * 8192, &tm_a, m0 + 64 * i, k0);
           } else {
-            tma_load_2d(a, &tm_a, &full[stage], k0, m0);
+            load(a, &tm_a, k0, m0);
           }
-          if constexpr (EPI == kEpiGateUp) {             // gate rows, then the matching up rows
-            tma_load_2d(b, &tm_b, &full[stage], k0, n0);
-            tma_load_2d(b + NT * BK * 2, &tm_b, &full[stage], k0, p.N + n0);
+          const int nb = n0 + static_cast<int>(rank) * C::B_ROWS;
+          if constexpr (EPI == kEpiGateUp && CG == 2) {  // gate rows in one CTA, the matching up rows in the other
+            load(b, &tm_b, k0, rank == 0 ? n0 : p.N + n0);
+          } else if constexpr (EPI == kEpiGateUp) {      // gate rows, then the matching up rows
+            load(b, &tm_b, k0, n0);
+            load(b + NT * BK * 2, &tm_b, k0, p.N + n0);
           } else if constexpr (B_MN) {
 #pragma unroll
-            for (int i = 0; i < BN / 64; ++i) tma_load_2d(b + i * 8192, &tm_b, &full[stage], n0 + 64 * i, k0);
+            for (int i = 0; i < C::B_ROWS / 64; ++i) load(b + i * 8192, &tm_b, nb + 64 * i, k0);
           } else {
-            tma_load_2d(b, &tm_b, &full[stage], k0, n0);
+            load(b, &tm_b, k0, nb);
           }
           armed |= 1u << stage;
           par = (par & ~(1u << stage)) | (phase << stage);
@@ -212,19 +234,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) {   // let every issued copy land before the CTA's shared memory is released
-        for (int s = 0; s < C::STAGES; ++s)
-          if (armed & (1u << s)) mbar_drain(&full[s], (par >> s) & 1u, kDrainNs);
+        for (int s = 0; s < C::STAGES; ++s)      // (rank 1 has no barrier of its own to watch: it waits the limit out)
+          if (armed & (1u << s)) mbar_drain(rank == 0 ? &full[s] : s_never, rank == 0 ? (par >> s) & 1u : 0u, kDrainNs);
       }
     }
   } else if (warp == WARP_MMA) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(CG * BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
       uint64_t* last_bar = nullptr;
       uint32_t last_par = 0;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
+      for (int tile = first; ok && tile < total; tile += step, ++it) {
         const int buf = it & 1;
         const uint32_t aphase = (it >> 1) & 1;
         if (!mbar_wait(&acc_empty[buf], aphase ^ 1u, wctx, 1201)) { ok = false; break; }
@@ -239,16 +261,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int kk = 0; kk < BK / 16; ++kk) {          // 16 of K: 32 bytes along a row, or two 8-row atoms
             const uint64_t da = A_MN ? smem_desc_mn_sw128(a0 + kk * 2048) : smem_desc_sw128(a0 + kk * 32);
             const uint64_t db = B_MN ? smem_desc_mn_sw128(b0 + kk * 2048) : smem_desc_sw128(b0 + kk * 32);
-            umma_bf16_ss(d, da, db, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+            if constexpr (CG == 2) umma_bf16_ss_pair(d, da, db, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+            else umma_bf16_ss(d, da, db, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
           }
-          umma_commit(&empty[stage]);
+          if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
+          else umma_commit(&empty[stage]);
           issued = true;
           last_bar = &empty[stage];
           last_par = phase;
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        umma_commit(&acc_full[buf]);
+        if constexpr (CG == 2) umma_commit_pair(&acc_full[buf]);
+        else umma_commit(&acc_full[buf]);
         last_bar = &acc_full[buf];
         last_par = aphase;
       }
@@ -258,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3;                        // TMEM lanes 32q..32q+31: D row = lane
     const int half = (warp - WARP_EPI0) >> 2;      // this warp's half of the columns
     int it = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
+    for (int tile = first; tile < total; tile += step, ++it) {
       int mt, nt;
       tile_at(p, tile, mt, nt);
       const int buf = it & 1;
@@ -266,7 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!mbar_wait_sleep(&acc_full[buf], aphase, wctx, 1401, 64)) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN);
-      const int row = mt * BM + 32 * q + lane;
+      const int row0 = (mt * CG + static_cast<int>(rank)) * BM + 32 * q;
+      const int row = row0 + lane;
       const bool row_in = row < p.M;
 #pragma unroll 1
       for (int c0 = half * (NT / 2); c0 < (half + 1) * (NT / 2); c0 += 16) {
@@ -356,11 +382,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           if (p.colsum) {                         // from the fp32 values, before their rounding to bf16
-            float* o = p.colsum + static_cast<int64_t>(mt * (BM / 32) + q) * 2 * p.N;
+            float* o = p.colsum + static_cast<int64_t>(row0 / 32) * 2 * p.N;
             int c;
             const float sg = warp_column_sum16(dg, lane, c);
             const float su = warp_column_sum16(du, lane, c);
-            if ((lane & 1) == 0 && col + c < p.N && mt * BM + 32 * q < p.M) {
+            if ((lane & 1) == 0 && col + c < p.N && row0 < p.M) {
               o[col + c] = sg;
               o[p.N + col + c] = su;
             }
@@ -369,24 +395,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        else mbar_arrive(&acc_empty[buf]);
+      }
     }
   }
 
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();         // neither CTA leaves while the other may still signal it
   if (warp == WARP_MMA) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
 }
 
 // ---------------------------------------------------------------------- host side
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
+template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
 e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
-  using C = Cfg<BN>;
-  auto kern = dense_gemm_kernel<BN, A_MN, B_MN, EPI>;
+  using C = Cfg<BN, CG>;
+  auto kern = dense_gemm_kernel<BN, CG, A_MN, B_MN, EPI>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [&] {
@@ -404,13 +435,14 @@ e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
   const bool ok_b = B_MN ? encode_tma_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.b, b_rows, g.K, b_rows * 2, 64, BK,
                                          CU_TENSOR_MAP_SWIZZLE_128B)
                          : encode_tma_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.b, g.K, b_rows,
-                                         static_cast<uint64_t>(g.K) * 2, BK, NT, CU_TENSOR_MAP_SWIZZLE_128B);
+                                         static_cast<uint64_t>(g.K) * 2, BK, EPI == kEpiGateUp ? NT : C::B_ROWS,
+                                         CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok_a || !ok_b) return E4B_ERR_CUDA;
   Params p;
   p.M = g.M;
   p.N = g.N;
   p.K = g.K;
-  p.m_tiles = (g.M + BM - 1) / BM;
+  p.m_tiles = (g.M + CG * BM - 1) / (CG * BM);
   p.n_tiles = (g.N + NT - 1) / NT;
   p.act = g.act;
   p.alpha = g.alpha;
@@ -426,14 +458,15 @@ e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
   p.clear_status = g.clear_status;
   p.wait_limit_ns = kWaitLimitNs;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  const int64_t sms = device_sm_count();
-  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(THREADS), C::SMEM_BYTES, s, ta,
-                    tb, p) == cudaSuccess
-             ? E4B_OK
-             : E4B_ERR_CUDA;
+  const int64_t slots = device_sm_count() / CG;
+  const dim3 grid(static_cast<unsigned>(CG * (tiles < slots ? tiles : slots)));
+  const cudaError_t e = CG == 2 ? launch_pdl_cluster(2, kern, grid, dim3(THREADS), C::SMEM_BYTES, s, ta, tb, p)
+                                : launch_pdl(kern, grid, dim3(THREADS), C::SMEM_BYTES, s, ta, tb, p);
+  return e == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
 
-// Widest tile that still gives every SM one; narrower ones spread a small product.
+// Pairs where every pair of SMs gets a 256 x 256 tile; else the widest single-CTA tile that
+// still gives every SM one: narrower ones spread a small product.
 template <bool A_MN, bool B_MN, int EPI>
 e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
   const int64_t mt = (g.M + BM - 1) / BM, sms = device_sm_count();
@@ -441,9 +474,9 @@ e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
     const int nt = EPI == kEpiGateUp ? bn / 2 : bn;
     return mt * ((g.N + nt - 1) / nt);
   };
-  if (tiles(256) >= sms) return launch_typed<256, A_MN, B_MN, EPI>(g, s);
-  if (tiles(128) >= sms) return launch_typed<128, A_MN, B_MN, EPI>(g, s);
-  return launch_typed<64, A_MN, B_MN, EPI>(g, s);
+  if ((mt + 1) / 2 * (tiles(256) / mt) >= sms / 2) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, s);
+  if (tiles(128) >= sms) return launch_typed<128, 1, A_MN, B_MN, EPI>(g, s);
+  return launch_typed<64, 1, A_MN, B_MN, EPI>(g, s);
 }
 
 }  // namespace

@@ -171,14 +171,15 @@ def header_functions():
 
 
 def _ptr(t):
-    if isinstance(t, Nf4DQ):         # host struct describing device arrays (E4B_NF4_DQ scales)
+    if type(t) is Nf4DQ:             # host struct describing device arrays (E4B_NF4_DQ scales)
         return ctypes.cast(ctypes.pointer(t), ctypes.c_void_p)
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # the handle without a Stream object
 
 
 def _check(status, where):
@@ -188,7 +189,7 @@ def _check(status, where):
 
 def _need_cuda(*ts):
     for t in ts:
-        if t is not None and not isinstance(t, Nf4DQ) and not t.is_cuda:
+        if t is not None and not getattr(t, "is_cuda", True):      # (an Nf4DQ was checked when it was made)
             raise ValueError("e4b: tensors must be CUDA tensors")
 
 
@@ -237,7 +238,7 @@ def e4b_route_workspace_bytes(T, E, k):
 def e4b_route(logits, T, E, k, gating, topk_ids, topk_w, expert_offsets, sorted_slot, ws, stream=None):
     _need_cuda(logits, topk_ids, topk_w, expert_offsets, sorted_slot, ws)
     _check(lib().e4b_route(_ptr(logits), T, E, k, gating, _ptr(topk_ids), _ptr(topk_w), _ptr(expert_offsets),
-                           _ptr(sorted_slot), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                           _ptr(sorted_slot), _ptr(ws), ws.nbytes, _stream(stream)),
            "e4b_route")
 
 
@@ -264,7 +265,7 @@ def e4b_moe_forward(desc, T, x, logits, gu_codes, gu_scales, dn_codes, dn_scales
     _need_cuda(x, logits, gu_codes, gu_scales, dn_codes, dn_scales, lora_A, lora_B, gu_bias, dn_bias, out, ws)
     _check(lib().e4b_moe_forward(ctypes.byref(desc), T, _ptr(x), _ptr(logits), _ptr(gu_codes), _ptr(gu_scales),
                                  _ptr(dn_codes), _ptr(dn_scales), _ptr(lora_A), _ptr(lora_B), _ptr(gu_bias),
-                                 _ptr(dn_bias), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
+                                 _ptr(dn_bias), _ptr(out), _ptr(ws), ws.nbytes,
                                  _stream(stream)), "e4b_moe_forward")
     return out
 
@@ -274,7 +275,7 @@ def e4b_moe_forward_stage(stage, desc, T, x, logits, gu_codes, gu_scales, dn_cod
     _check(lib().e4b_moe_forward_stage(stage, ctypes.byref(desc), T, _ptr(x), _ptr(logits), _ptr(gu_codes),
                                        _ptr(gu_scales), _ptr(dn_codes), _ptr(dn_scales), _ptr(lora_A), _ptr(lora_B),
                                        _ptr(gu_bias), _ptr(dn_bias), _ptr(out), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _stream(stream)),
+                                       ws.nbytes, _stream(stream)),
            "e4b_moe_forward_stage")
     return out
 
@@ -289,7 +290,7 @@ def e4b_moe_forward_train(desc, T, x, logits, gu_codes, gu_scales, dn_codes, dn_
     _check(lib().e4b_moe_forward_train(ctypes.byref(desc), T, _ptr(x), _ptr(logits), _ptr(gu_codes),
                                        _ptr(gu_scales), _ptr(dn_codes), _ptr(dn_scales), _ptr(lora_A),
                                        _ptr(lora_B), _ptr(gu_bias), _ptr(dn_bias), _ptr(out), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _stream(stream)), "e4b_moe_forward_train")
+                                       ws.nbytes, _stream(stream)), "e4b_moe_forward_train")
     return out
 
 
@@ -298,7 +299,7 @@ def e4b_moe_backward(desc, T, logits, dout, gu_codes, gu_scales, dn_codes, dn_sc
     _need_cuda(logits, dout, gu_codes, gu_scales, dn_codes, dn_scales, lora_A, lora_B, dx, dlogits, dA, dB, ws)
     _check(lib().e4b_moe_backward(ctypes.byref(desc), T, _ptr(logits), _ptr(dout), _ptr(gu_codes), _ptr(gu_scales),
                                   _ptr(dn_codes), _ptr(dn_scales), _ptr(lora_A), _ptr(lora_B), _ptr(dx),
-                                  _ptr(dlogits), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel() * ws.element_size(),
+                                  _ptr(dlogits), _ptr(dA), _ptr(dB), _ptr(ws), ws.nbytes,
                                   _stream(stream)), "e4b_moe_backward")
     return dx, dlogits, dA, dB
 
@@ -316,7 +317,7 @@ def e4b_rmsnorm_backward_workspace_bytes(T, H):
 def e4b_rmsnorm_backward(dy, dy_type, dr, r, weight, rstd, T, H, dx, dweight, ws, stream=None):
     _need_cuda(dy, dr, r, weight, rstd, dx, dweight, ws)
     _check(lib().e4b_rmsnorm_backward(_ptr(dy), dy_type, _ptr(dr), _ptr(r), _ptr(weight), _ptr(rstd), T, H, _ptr(dx),
-                                      _ptr(dweight), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                      _ptr(dweight), _ptr(ws), ws.nbytes, _stream(stream)),
            "e4b_rmsnorm_backward")
     return dx, dweight
 
@@ -332,7 +333,7 @@ def e4b_ffn_train_workspace_bytes(desc, T):
 def e4b_ffn_forward(desc, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, stream=None):
     _need_cuda(x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws)
     _check(lib().e4b_ffn_forward(ctypes.byref(desc), T, _ptr(x), _ptr(w_gu), _ptr(w_dn), _ptr(gu_bias), _ptr(dn_bias),
-                                 _ptr(add), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                 _ptr(add), _ptr(out), _ptr(ws), ws.nbytes, _stream(stream)),
            "e4b_ffn_forward")
     return out
 
@@ -340,7 +341,7 @@ def e4b_ffn_forward(desc, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, stre
 def e4b_ffn_forward_train(desc, T, x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws, stream=None):
     _need_cuda(x, w_gu, w_dn, gu_bias, dn_bias, add, out, ws)
     _check(lib().e4b_ffn_forward_train(ctypes.byref(desc), T, _ptr(x), _ptr(w_gu), _ptr(w_dn), _ptr(gu_bias),
-                                       _ptr(dn_bias), _ptr(add), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
+                                       _ptr(dn_bias), _ptr(add), _ptr(out), _ptr(ws), ws.nbytes,
                                        _stream(stream)), "e4b_ffn_forward_train")
     return out
 
@@ -349,7 +350,7 @@ def e4b_ffn_backward(desc, T, x, dout, w_gu, w_dn, dx, dw_gu, dw_dn, dgu_bias, d
     _need_cuda(x, dout, w_gu, w_dn, dx, dw_gu, dw_dn, dgu_bias, ddn_bias, ws)
     _check(lib().e4b_ffn_backward(ctypes.byref(desc), T, _ptr(x), _ptr(dout), _ptr(w_gu), _ptr(w_dn), _ptr(dx),
                                   _ptr(dw_gu), _ptr(dw_dn), _ptr(dgu_bias), _ptr(ddn_bias), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)), "e4b_ffn_backward")
+                                  ws.nbytes, _stream(stream)), "e4b_ffn_backward")
     return dx, dw_gu, dw_dn, dgu_bias, ddn_bias
 
 
@@ -361,7 +362,7 @@ def e4b_clip_grad_norm(grads, max_norm, total_norm, ws, stream=None):
     """grads: the array of :func:`make_grads`."""
     _need_cuda(total_norm, ws)
     _check(lib().e4b_clip_grad_norm(ctypes.cast(grads, ctypes.c_void_p), len(grads), max_norm, _ptr(total_norm),
-                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "e4b_clip_grad_norm")
+                                    _ptr(ws), ws.nbytes, _stream(stream)), "e4b_clip_grad_norm")
     return total_norm
 
 
@@ -371,5 +372,5 @@ def e4b_device_status(ws, stream=None):
 
 
 def e4b_debug_wait_timeout(limit_ns, ws, stream=None):
-    _check(lib().e4b_debug_wait_timeout(limit_ns, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+    _check(lib().e4b_debug_wait_timeout(limit_ns, _ptr(ws), ws.nbytes, _stream(stream)),
            "e4b_debug_wait_timeout")

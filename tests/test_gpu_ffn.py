@@ -91,7 +91,9 @@ class Case:
 # tile width, and enough columns for the widest tile
 SHAPES = [(1, 8, 8), (1, 2048, 768), (2, 64, 128), (7, 72, 200), (8, 264, 40), (9, 2048, 768), (16, 136, 1000),
           (17, 8, 8), (17, 64, 128), (31, 72, 200), (32, 200, 72), (33, 264, 776), (127, 512, 64), (128, 64, 512),
-          (129, 128, 136), (300, 520, 296), (1000, 136, 2440), (700, 1400, 2808), (2050, 264, 1160)]
+          (129, 128, 136), (300, 520, 296), (1000, 136, 2440), (700, 1400, 2808), (2050, 264, 1160),
+          # each product of the pair in turn on CTA pairs, with ragged rows and columns
+          (2050, 72, 2312), (2050, 2312, 72), (40, 2568, 2008)]
 
 
 @pytest.mark.parametrize("T,H,I", SHAPES)
