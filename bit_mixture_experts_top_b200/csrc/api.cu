@@ -590,7 +590,7 @@ e4b_status e4b_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
 
 size_t e4b_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H) {
   if (T < 0 || H < 1) return 0;
-  return align_up(static_cast<size_t>(norm_backward_blocks(T)) * H * 4);
+  return kStatusBytes + align_up(static_cast<size_t>(norm_backward_blocks(T)) * H * 4);
 }
 
 e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t* dr, const uint16_t* r,
@@ -615,7 +615,7 @@ e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t*
       return E4B_ERR_INVALID_ARG;
   if (overlap(odx, odw) || overlap(odx, w) || overlap(odw, w)) return E4B_ERR_INVALID_ARG;
   const NormBackwardLaunch p{dy, dy_type == E4B_F32 ? 1 : 0, dr, r, weight, rstd, T, H, 1.0 / H, dx, dweight,
-                             static_cast<float*>(ws)};
+                             at<float>(ws, kStatusBytes), static_cast<int32_t*>(ws)};
   return launch_rmsnorm_backward(p, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
 

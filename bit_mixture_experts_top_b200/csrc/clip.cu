@@ -50,7 +50,8 @@ struct ClipTable {
   ClipEntry e[N];
 };
 
-__device__ __forceinline__ int type_bytes(int type) { return type == E4B_F32 ? 4 : 2; }
+template <int TYPE>
+__host__ __device__ constexpr int size_of() { return TYPE == E4B_F32 ? 4 : 2; }
 
 template <int N>
 __device__ __forceinline__ int tensor_of(const ClipTable<N>& t, int chunk) {
@@ -63,16 +64,14 @@ __device__ __forceinline__ int tensor_of(const ClipTable<N>& t, int chunk) {
 }
 
 // The elements of one 16-byte word as fp32.
-__device__ __forceinline__ int word_values(const uint4& v, int type, float (&f)[8]) {
+template <int TYPE>
+__device__ __forceinline__ void word_values(const uint4& v, float (&f)[16 / size_of<TYPE>()]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if (type == E4B_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
-    return 4;
-  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (type == E4B_BF16) {
+    if constexpr (TYPE == E4B_F32) {
+      f[i] = __uint_as_float(w[i]);
+    } else if constexpr (TYPE == E4B_BF16) {
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     } else {
@@ -81,28 +80,111 @@ __device__ __forceinline__ int word_values(const uint4& v, int type, float (&f)[
       f[2 * i + 1] = h.y;
     }
   }
-  return 8;
 }
 
-__device__ __forceinline__ uint32_t two_halves(float lo, float hi, int type) {
-  if (type == E4B_BF16) {
+template <int TYPE>
+__device__ __forceinline__ uint32_t two_halves(float lo, float hi) {
+  if constexpr (TYPE == E4B_BF16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ float load_one(const void* p, int64_t i, int type) {
-  if (type == E4B_F32) return static_cast<const float*>(p)[i];
-  if (type == E4B_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+template <int TYPE>
+__device__ __forceinline__ uint4 scaled_word(const uint4& v, float c) {
+  float f[16 / size_of<TYPE>()];
+  word_values<TYPE>(v, f);
+  if constexpr (TYPE == E4B_F32)
+    return make_uint4(__float_as_uint(f[0] * c), __float_as_uint(f[1] * c), __float_as_uint(f[2] * c),
+                      __float_as_uint(f[3] * c));
+  else
+    return make_uint4(two_halves<TYPE>(f[0] * c, f[1] * c), two_halves<TYPE>(f[2] * c, f[3] * c),
+                      two_halves<TYPE>(f[4] * c, f[5] * c), two_halves<TYPE>(f[6] * c, f[7] * c));
 }
 
-__device__ __forceinline__ void store_one(void* p, int64_t i, int type, float v) {
-  if (type == E4B_F32) static_cast<float*>(p)[i] = v;
-  else if (type == E4B_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+template <int TYPE>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+  if constexpr (TYPE == E4B_F32) return static_cast<const float*>(p)[i];
+  else if constexpr (TYPE == E4B_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  else return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
+  if constexpr (TYPE == E4B_F32) static_cast<float*>(p)[i] = v;
+  else if constexpr (TYPE == E4B_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Calls word(i) for this thread's words of the chunk that lie wholly inside the
+// tensor and one(k) for the single elements of its first and last word.  A
+// chunk in the tensor's middle is only whole words and takes no tests.
+template <int TYPE, typename Word, typename One>
+__device__ __forceinline__ void for_chunk(const ClipEntry& e, int64_t w0, const Word& word, const One& one) {
+  constexpr int PER = 16 / size_of<TYPE>();
+  const int64_t last = e.n + e.skip;                      // elements counted from the first word's start
+  const int64_t c0 = w0 - threadIdx.x;
+  if (c0 * PER >= e.skip && (c0 + kChunkVecs) * PER <= last) {
+    uint4 v[kVecPerThread];
+    const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>()) + w0;
+#pragma unroll
+    for (int i = 0; i < kVecPerThread; ++i) v[i] = in[i * kThreads];
+#pragma unroll
+    for (int i = 0; i < kVecPerThread; ++i) word(w0 + i * kThreads, v[i]);
+    return;
+  }
+  const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>());
+  for (int i = 0; i < kVecPerThread; ++i) {
+    const int64_t w = w0 + i * kThreads, at = w * PER;
+    if (at >= last) break;
+    if (at >= e.skip && at + PER <= last) {
+      word(w, in[w]);
+    } else {
+      for (int j = 0; j < PER; ++j)
+        if (at + j >= e.skip && at + j < last) one(at + j - e.skip);
+    }
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ double chunk_squares(const ClipEntry& e, int64_t w0) {
+  double sum = 0.0;
+  for_chunk<TYPE>(
+      e, w0,
+      [&](int64_t, const uint4& v) {
+        float f[16 / size_of<TYPE>()];
+        word_values<TYPE>(v, f);
+#pragma unroll
+        for (int j = 0; j < 16 / size_of<TYPE>(); ++j)
+          sum = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), sum);
+      },
+      [&](int64_t k) {
+        const double g = load_one<TYPE>(e.in, k);
+        sum = fma(g, g, sum);
+      });
+  return sum;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void chunk_scale(const ClipEntry& e, int64_t w0, float c) {
+  constexpr int PER = 16 / size_of<TYPE>();
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(e.out) - e.skip * size_of<TYPE>());
+  for_chunk<TYPE>(
+      e, w0,
+      [&](int64_t w, const uint4& v) {
+        if (e.words) {
+          __stcs(out + w, scaled_word<TYPE>(v, c));
+        } else {
+          float f[PER];
+          word_values<TYPE>(v, f);
+#pragma unroll
+          for (int j = 0; j < PER; ++j) store_one<TYPE>(e.out, w * PER + j - e.skip, f[j] * c);
+        }
+      },
+      [&](int64_t k) { store_one<TYPE>(e.out, k, load_one<TYPE>(e.in, k) * c); });
 }
 
 __device__ __forceinline__ double block_sum(double v, double* red) {
@@ -129,34 +211,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   for (int c = c0; c < c1; ++c) {
     while (ti + 1 < t.tensors && t.e[ti + 1].chunk0 <= c) ++ti;
     const ClipEntry& e = t.e[ti];
-    const int type = e.type, per = 16 / type_bytes(type);
-    const uint8_t* base = static_cast<const uint8_t*>(e.in) - e.skip * type_bytes(type);
     const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * kChunkVecs + threadIdx.x;
-    const int64_t last = e.n + e.skip;     // elements counted from the first word's start
-    uint4 v[kVecPerThread];
-#pragma unroll
-    for (int i = 0; i < kVecPerThread; ++i) {
-      const int64_t at = (w0 + i * kThreads) * per;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (at >= e.skip && at + per <= last) v[i] = *reinterpret_cast<const uint4*>(base + (w0 + i * kThreads) * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kVecPerThread; ++i) {
-      const int64_t at = (w0 + i * kThreads) * per;
-      if (at >= e.skip && at + per <= last) {
-        float f[8];
-        const int m = word_values(v[i], type, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < m) sum = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), sum);
-      } else if (at < last) {              // the first or last word, not wholly the tensor's
-        for (int j = 0; j < per; ++j)
-          if (at + j >= e.skip && at + j < last) {
-            const double g = load_one(e.in, at + j - e.skip, type);
-            sum = fma(g, g, sum);
-          }
-      }
-    }
+    if (e.type == E4B_F32) sum += chunk_squares<E4B_F32>(e, w0);
+    else if (e.type == E4B_BF16) sum += chunk_squares<E4B_BF16>(e, w0);
+    else sum += chunk_squares<E4B_F16>(e, w0);
   }
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -184,46 +242,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
     while (t.e[ti].chunk0 > c) --ti;
     const ClipEntry& e = t.e[ti];
     if (e.in == e.out && coef == 1.0f) continue;          // in place and unclipped: already there
-    const int type = e.type, size = type_bytes(type), per = 16 / size;
-    const uint8_t* base = static_cast<const uint8_t*>(e.in) - e.skip * size;
-    uint8_t* obase = static_cast<uint8_t*>(e.out) - e.skip * size;
     const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * kChunkVecs + threadIdx.x;
-    const int64_t last = e.n + e.skip;
-    uint4 v[kVecPerThread];
-#pragma unroll
-    for (int i = 0; i < kVecPerThread; ++i) {
-      const int64_t at = (w0 + i * kThreads) * per;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (at >= e.skip && at + per <= last) v[i] = *reinterpret_cast<const uint4*>(base + (w0 + i * kThreads) * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kVecPerThread; ++i) {
-      const int64_t at = (w0 + i * kThreads) * per;
-      if (at >= e.skip && at + per <= last) {
-        float f[8];
-        word_values(v[i], type, f);
-        if (e.words) {
-          uint4 o;
-          if (type == E4B_F32)
-            o = make_uint4(__float_as_uint(f[0] * coef), __float_as_uint(f[1] * coef), __float_as_uint(f[2] * coef),
-                           __float_as_uint(f[3] * coef));
-          else
-            o = make_uint4(two_halves(f[0] * coef, f[1] * coef, type), two_halves(f[2] * coef, f[3] * coef, type),
-                           two_halves(f[4] * coef, f[5] * coef, type), two_halves(f[6] * coef, f[7] * coef, type));
-          __stcs(reinterpret_cast<uint4*>(obase + (w0 + i * kThreads) * 16), o);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < per) store_one(e.out, at + j - e.skip, type, f[j] * coef);
-        }
-      } else if (at < last) {
-        for (int j = 0; j < per; ++j)
-          if (at + j >= e.skip && at + j < last) {
-            const int64_t k = at + j - e.skip;
-            store_one(e.out, k, type, load_one(e.in, k, type) * coef);
-          }
-      }
-    }
+    if (e.type == E4B_F32) chunk_scale<E4B_F32>(e, w0, coef);
+    else if (e.type == E4B_BF16) chunk_scale<E4B_BF16>(e, w0, coef);
+    else chunk_scale<E4B_F16>(e, w0, coef);
   }
 }
 

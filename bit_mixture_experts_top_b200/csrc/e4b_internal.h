@@ -207,6 +207,7 @@ struct NormBackwardLaunch {
   uint16_t* dx;
   float* dweight;
   float* partial;                          // [norm_backward_blocks(T), H]
+  int32_t* status;
 };
 int norm_backward_blocks(int32_t T);
 cudaError_t launch_rmsnorm_backward(const NormBackwardLaunch& p, cudaStream_t s);

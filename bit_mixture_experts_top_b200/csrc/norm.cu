@@ -25,6 +25,8 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
 
@@ -33,6 +35,9 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kMaxWarps = 32;
+constexpr int kBackThreads = 512, kBackGroups = 15;   // backward: a block's threads, and its groups (one named barrier each)
+constexpr int kSlotBytes = 208 * 1024;                // and the shared memory of its row slots
+constexpr int kManyRowsPerSm = 16;   // from so many rows per SM on, fewer threads take a row
 
 __device__ __forceinline__ float bf16_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
@@ -114,8 +119,54 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t amax_bits) {
 // 2^(127 - byte) as fp32, exact (a finite block's byte is at most 247).
 __device__ __forceinline__ float mx_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
+__device__ __forceinline__ uint2 codes8(const float (&f)[8]) {
+  return make_uint2(e4m3x2(f[0], f[1]) | (static_cast<uint32_t>(e4m3x2(f[2], f[3])) << 16),
+                    e4m3x2(f[4], f[5]) | (static_cast<uint32_t>(e4m3x2(f[6], f[7])) << 16));
+}
+
+// Byte of the 32-value block that four adjacent lanes hold, from each lane's own maximum.
+__device__ __forceinline__ uint32_t block_byte(uint32_t m) {
+  m = max(m, __shfl_xor_sync(kFull, m, 1));
+  m = max(m, __shfl_xor_sync(kFull, m, 2));
+  return mx_byte(m);
+}
+
+__device__ __forceinline__ uint2 mx_codes(const float (&f)[8], uint32_t byte) {
+  if (byte == 255u) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const float s = mx_inverse(byte);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = f[j] * s;
+  return codes8(v);
+}
+
+__device__ __forceinline__ uint2 row_codes(const float (&f)[8], float s, uint32_t amax_bits) {
+  if (amax_bits >= kInfBits) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  // fl32(f / s) by Markstein's correction of f * RN(1/s), as in the NF4 quantiser; a tiny scale is lifted
+  // with its values by 2^96 so that the residual stays normal (quotients that underflow have code 0 anyway)
+  const float up = s < 0x1p-60f ? 0x1p96f : 1.0f;
+  const float a = s * up, r = __frcp_rn(a);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = f[j] * up, q = x * r;
+    v[j] = copysignf(fmaf(fmaf(-a, q, x), r, q), x);   // (the correction would turn -0 into 0)
+  }
+  return codes8(v);
+}
+
+// fl32(1 / sqrt(v)): an fp32 estimate refined by two Newton steps in fp64,
+// y <- y (1.5 - 0.5 v y^2), which leave a few units of 2^-53; far cheaper per
+// thread than the fp64 root and quotient.  Zero, infinite, NaN and very small or
+// large v take those.
 __device__ __forceinline__ float rstd_of(double sum, double inv_h, double eps) {
-  return static_cast<float>(1.0 / sqrt(sum * inv_h + eps));
+  const double v = sum * inv_h + eps;
+  if (!(v > 1e-30 && v < 1e30)) return static_cast<float>(1.0 / sqrt(v));
+  double y = static_cast<double>(rsqrtf(static_cast<float>(v)));
+  const double half = 0.5 * v;
+  y = y * fma(-half * y, y, 1.5);
+  y = y * fma(-half * y, y, 1.5);
+  return static_cast<float>(y);
 }
 
 // ---------------------------------------------------------------------- forward
@@ -174,17 +225,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch p) {
       if (v < nvec) m = max(m, abs_bits(f[j]));   // outside the row 0 * rstd may be NaN
     }
     if (p.y && v < nvec) reinterpret_cast<uint4*>(p.y + row * p.H)[v] = pack8(f);
-    if (p.q_format == E4B_Q8_MX) {   // the four lanes of one 32-value block
-      m = max(m, __shfl_xor_sync(kFull, m, 1));
-      m = max(m, __shfl_xor_sync(kFull, m, 2));
-      const uint32_t byte = mx_byte(m);
-      const float s = mx_inverse(byte);
-      uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      if (byte != 255u)
-        q = make_uint2(e4m3x2(f[0] * s, f[1] * s) | (static_cast<uint32_t>(e4m3x2(f[2] * s, f[3] * s)) << 16),
-                       e4m3x2(f[4] * s, f[5] * s) | (static_cast<uint32_t>(e4m3x2(f[6] * s, f[7] * s)) << 16));
+    if (p.q_format == E4B_Q8_MX) {
+      const uint32_t byte = block_byte(m);
       if (v < nvec) {
-        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = q;
+        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = mx_codes(f, byte);
         if ((v & 3) == 0) static_cast<uint8_t*>(p.q_scales)[row * (p.H >> 5) + (v >> 2)] = static_cast<uint8_t>(byte);
       }
     }
@@ -201,14 +245,96 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch p) {
       float f[8], w[8];
       unpack8(raw[i], f);
       unpack8(wv[i], w);
-      uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      if (amax < kInfBits) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j] * rstd * w[j], s);
-        q = make_uint2(e4m3x2(f[0], f[1]) | (static_cast<uint32_t>(e4m3x2(f[2], f[3])) << 16),
-                       e4m3x2(f[4], f[5]) | (static_cast<uint32_t>(e4m3x2(f[6], f[7])) << 16));
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
+      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = row_codes(f, s, amax);
+    }
+  }
+}
+
+// One warp per row, VPT vectors of eight values per lane: for many rows the
+// reduction is five shuffles and no barrier, and the statistics are formed once
+// per 8 VPT values of a lane.  The weights come from L1 when they are used.
+template <int VPT>
+__global__ void __launch_bounds__(128) norm_warp_kernel(const NormLaunch p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= p.T) return;
+  const int nvec = p.H >> 3;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
+  uint4 raw[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) raw[i] = 32 * i + lane < nvec ? x[32 * i + lane] : make_uint4(0, 0, 0, 0);
+  double sum = 0.0;
+  if (p.residual) {
+    const uint4* res = reinterpret_cast<const uint4*>(p.residual + row * p.H);
+    uint4 add[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) add[i] = 32 * i + lane < nvec ? res[32 * i + lane] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float f[8], a[8];
+      unpack8(raw[i], f);
+      unpack8(add[i], a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += a[j];
+      raw[i] = pack8(f);
+      if (p.r_out && 32 * i + lane < nvec) reinterpret_cast<uint4*>(p.r_out + row * p.H)[32 * i + lane] = raw[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float f[8];
+    unpack8(raw[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += static_cast<double>(f[j] * f[j]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  const float rstd = rstd_of(sum, p.inv_h, p.eps);
+  if (p.rstd && lane == 0) p.rstd[row] = rstd;
+  const uint4* weight = reinterpret_cast<const uint4*>(p.weight);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = 32 * i + lane;
+    const bool in = v < nvec;
+    float f[8], w[8];
+    unpack8(raw[i], f);
+    unpack8(in ? __ldg(weight + v) : make_uint4(0, 0, 0, 0), w);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = f[j] * rstd * w[j];
+      m = max(m, abs_bits(f[j]));
+    }
+    if (!in) m = 0;                                // outside the row 0 * rstd may be NaN
+    if (p.y && in) reinterpret_cast<uint4*>(p.y + row * p.H)[v] = pack8(f);
+    if (p.q_format == E4B_Q8_MX) {
+      const uint32_t byte = block_byte(m);
+      if (in) {
+        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = mx_codes(f, byte);
+        if ((v & 3) == 0) static_cast<uint8_t*>(p.q_scales)[row * (p.H >> 5) + (v >> 2)] = static_cast<uint8_t>(byte);
       }
-      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = q;
+    }
+    amax = max(amax, m);
+  }
+  if (p.q_format == E4B_Q8_ROW) {
+    amax = __reduce_max_sync(kFull, amax);
+    const float s = row_scale(amax);
+    if (lane == 0) static_cast<float*>(p.q_scales)[row] = s;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = 32 * i + lane;
+      if (v >= nvec) continue;
+      float f[8], w[8];
+      unpack8(raw[i], f);
+      unpack8(__ldg(weight + v), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
+      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = row_codes(f, s, amax);
     }
   }
 }
@@ -264,109 +390,156 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormLaunch p) {
 
 // ---------------------------------------------------------------------- backward
 
-template <typename DY>
-__device__ __forceinline__ void load_dy8(const void* dy, int64_t vec, float (&f)[8]) {
-  if constexpr (sizeof(DY) == 4) {
-    const float4* p = static_cast<const float4*>(dy) + 2 * vec;
-    const float4 a = p[0], b = p[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    unpack8(static_cast<const uint4*>(dy)[vec], f);
+// Rows are dealt to groups of `tx` threads, several per block; a thread owns
+// VPT vectors of eight columns and keeps their weight gradient in registers over
+// all its rows, so dw costs one row of partial sums per block.  One thread of a
+// group brings its next STAGES rows into shared memory by bulk copies (whole
+// rows are contiguous), which keeps HBM busy whatever the group computes; what a
+// row costs beside its values (the waits, the row sum over the group) is paid
+// once per 8 VPT values of a thread.
+template <typename DY, int VPT, int STAGES>
+__global__ void __launch_bounds__(kBackThreads, 1) norm_backward_kernel(const NormBackwardLaunch p, int tx) {
+  constexpr int DYV = sizeof(DY) / 2;                   // 16-byte words of dy per vector
+  extern __shared__ uint4 slots[];                      // [group][stage][dy row | r row | dr row], then the weights
+  __shared__ float red[2][kBackGroups][16];
+  __shared__ uint64_t full[kBackGroups][STAGES];
+  __shared__ int32_t abort_flag;
+  const int nvec = p.H >> 3, g = threadIdx.x / tx, t = threadIdx.x - g * tx, groups = blockDim.x / tx;
+  const int nw = tx >> 5, warp = t >> 5, lane = threadIdx.x & 31;
+  const int row_words = (DYV + (p.dr ? 2 : 1)) * nvec;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  uint4* mine = slots + static_cast<int64_t>(g) * STAGES * row_words;
+  uint4* wsm = slots + static_cast<int64_t>(groups) * STAGES * row_words;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < groups; ++i)
+      for (int s = 0; s < STAGES; ++s) mbar_init(&full[i][s], 1);
+    abort_flag = 0;
+    fence_mbar_init();
   }
-}
-
-// Blocks walk groups of ROWS rows; a thread owns VPT vectors of eight columns
-// and keeps their weight gradient in registers over all its rows, so dw costs
-// one row of partial sums per block.  ROWS rows are loaded together and share
-// one reduction: that many times the bytes in flight per barrier.
-template <typename DY, int VPT, int ROWS>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardLaunch p) {
-  __shared__ float red[2][ROWS][16];
   pdl_wait();
   pdl_launch_dependents();
-  const int nvec = p.H >> 3, nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;   // (a wait can only run out seconds later)
+  for (int v = threadIdx.x; v < nvec; v += blockDim.x) wsm[v] = __ldg(reinterpret_cast<const uint4*>(p.weight) + v);
+  __syncthreads();
+  const WaitCtx wctx{&abort_flag, p.status, kWaitLimitNs};
+  const uint4* dyp = static_cast<const uint4*>(p.dy);
+  const uint4* rp = reinterpret_cast<const uint4*>(p.r);
+  const uint4* drp = reinterpret_cast<const uint4*>(p.dr);
+  auto fetch = [&](int64_t row, int stage) {            // by the group's first thread
+    if (row >= p.T) return;
+    uint4* d = mine + stage * row_words;
+    mbar_arrive_expect_tx(&full[g][stage], 16u * row_words);
+    bulk_load(d, dyp + row * DYV * nvec, 16u * DYV * nvec, &full[g][stage]);
+    bulk_load(d + DYV * nvec, rp + row * nvec, 16u * nvec, &full[g][stage]);
+    if (drp) bulk_load(d + (DYV + 1) * nvec, drp + row * nvec, 16u * nvec, &full[g][stage]);
+  };
   float dw[VPT][8];
-  uint4 wv[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    wv[i] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.weight) + v) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  }
   const float inv_h = static_cast<float>(p.inv_h);
-  int buf = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * ROWS; r0 < p.T; r0 += static_cast<int64_t>(gridDim.x) * ROWS) {
-    float dy[ROWS][VPT][8];
-    uint4 rr[ROWS][VPT], dr[ROWS][VPT];
-    float rs[ROWS];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + g;
+  if (t == 0)
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const bool row_in = r0 + k < p.T;
-      rs[k] = row_in ? __ldg(p.rstd + r0 + k) : 0.0f;
+    for (int s = 0; s < STAGES; ++s) fetch(first + s * step, s);
+  int buf = 0, stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;               // after a wait that ran out the thread keeps the group's barriers company, no more
+  for (int64_t row = first; row < p.T; row += step) {
+    const float rs = __ldg(p.rstd + row);
+    ok = ok && mbar_wait(&full[g][stage], phase, wctx, 2101);
+    float a[VPT][8], c = 0.0f;
+    uint4 rr[VPT];
+    const uint4* d = mine + stage * row_words;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
-        const int64_t vec = (r0 + k) * nvec + v;
-        rr[k][i] = dr[k][i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * tx + t;
+      rr[i] = make_uint4(0, 0, 0, 0);
+      if (v >= nvec || !ok) break;
+      if constexpr (DYV == 2) {
+        const uint4 lo = d[2 * v], hi = d[2 * v + 1];
+        a[i][0] = __uint_as_float(lo.x); a[i][1] = __uint_as_float(lo.y);
+        a[i][2] = __uint_as_float(lo.z); a[i][3] = __uint_as_float(lo.w);
+        a[i][4] = __uint_as_float(hi.x); a[i][5] = __uint_as_float(hi.y);
+        a[i][6] = __uint_as_float(hi.z); a[i][7] = __uint_as_float(hi.w);
+      } else {
+        unpack8(d[v], a[i]);
+      }
+      rr[i] = d[DYV * nvec + v];
+      float r[8], w[8];
+      unpack8(rr[i], r);
+      unpack8(wsm[v], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dy[k][i][j] = 0.0f;
-        if (row_in && v < nvec) {
-          load_dy8<DY>(p.dy, vec, dy[k][i]);
-          rr[k][i] = reinterpret_cast<const uint4*>(p.r)[vec];
-          if (p.dr) dr[k][i] = reinterpret_cast<const uint4*>(p.dr)[vec];
-        }
+      for (int j = 0; j < 8; ++j) {
+        const float xh = r[j] * rs;
+        dw[i][j] = fmaf(a[i][j], xh, dw[i][j]);
+        a[i][j] *= w[j];
+        c = fmaf(a[i][j], xh, c);
       }
     }
-    float c[ROWS];
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      c[k] = 0.0f;
+    for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(kFull, c, off);
+    if (nw > 1) {                                       // the group's warps, through shared memory
+      if (lane == 0) red[buf][g][warp] = c;
+      asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(tx) : "memory");
+      c = red[buf][g][0];
+      for (int w = 1; w < nw; ++w) c += red[buf][g][w];
+      buf ^= 1;   // a warp may be one row ahead of the slowest reader, never two
+    } else {
+      __syncwarp();
+    }
+    // every thread of the group is past the row before: its slot takes the row STAGES after it
+    if (STAGES > 1 && t == 0 && ok && row != first)
+      fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    const float k = c * inv_h * rs;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float r[8], w[8];
-        unpack8(rr[k][i], r);
-        unpack8(wv[i], w);
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * tx + t;
+      if (v >= nvec || !ok) break;
+      float r[8], o[8];
+      unpack8(rr[i], r);
+      if (drp) {
+        unpack8(d[(DYV + 1) * nvec + v], o);
+      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xh = r[j] * rs[k];
-          dw[i][j] = fmaf(dy[k][i][j], xh, dw[i][j]);
-          c[k] = fmaf(dy[k][i][j] * w[j], xh, c[k]);
-        }
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
       }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) c[k] += __shfl_xor_sync(kFull, c[k], off);
-      if (lane == 0) red[buf][k][warp] = c[k];
+      for (int j = 0; j < 8; ++j) o[j] = fmaf(rs, fmaf(-r[j], k, a[i][j]), o[j]);
+      reinterpret_cast<uint4*>(p.dx)[row * nvec + v] = pack8(o);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      float s = red[buf][k][0];
-      for (int w = 1; w < nw; ++w) s += red[buf][k][w];
-      s *= inv_h;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
-        if (r0 + k >= p.T || v >= nvec) continue;
-        float r[8], w[8], d[8];
-        unpack8(rr[k][i], r);
-        unpack8(wv[i], w);
-        unpack8(dr[k][i], d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += rs[k] * (dy[k][i][j] * w[j] - r[j] * rs[k] * s);
-        reinterpret_cast<uint4*>(p.dx)[(r0 + k) * nvec + v] = pack8(d);
-      }
+    if constexpr (STAGES == 1) {                        // the only slot: wait for the row's last reader
+      asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(tx) : "memory");
+      if (t == 0 && ok) fetch(row + step, 0);
     }
-    buf ^= 1;   // a warp may be one group ahead of the slowest reader, never two
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
   }
+  if (!ok && t == 0)            // let copies in flight land before the shared memory is used or released
+    for (int s = 0; s < STAGES; ++s) mbar_drain(&full[g][s], phase ^ (s < stage ? 1u : 0u), 50000000ull);
+  __syncthreads();
+  // the groups' weight gradients, added in order
+  float4* sum = reinterpret_cast<float4*>(slots);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    if (v >= nvec) continue;
-    float4* o = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(blockIdx.x) * p.H) + 2 * v;
-    o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-    o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    const int v = i * tx + t;
+    if (v >= nvec) break;
+    sum[static_cast<int64_t>(2 * g) * nvec + v] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+    sum[static_cast<int64_t>(2 * g + 1) * nvec + v] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+  }
+  __syncthreads();
+  float4* out = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(blockIdx.x) * p.H);
+  for (int v = threadIdx.x; v < 2 * nvec; v += blockDim.x) {
+    const int half = v & 1, at = v >> 1;
+    float4 s = sum[static_cast<int64_t>(half) * nvec + at];
+    for (int h = 1; h < groups; ++h) {
+      const float4 o = sum[static_cast<int64_t>(2 * h + half) * nvec + at];
+      s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+    }
+    out[v] = s;
   }
 }
 
@@ -382,6 +555,7 @@ template <typename DY>
 __global__ void __launch_bounds__(128) norm_dw_any_kernel(const NormBackwardLaunch p) {
   pdl_wait();
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
   const int h = blockIdx.x * blockDim.x + threadIdx.x;
   if (h >= p.H) return;
   float dw = 0.0f;
@@ -414,17 +588,36 @@ int threads_for(int H, int vpt) {
   return ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
 }
 
+template <typename DY, int VPT, int STAGES>
+cudaError_t launch_backward_vec(const NormBackwardLaunch& p, int blocks, cudaStream_t s) {
+  auto kern = norm_backward_kernel<DY, VPT, STAGES>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [&] {
+    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  // as many groups as threads, barriers and shared memory allow; their weight gradients (4 H bytes each) reuse
+  // the slots, which are never smaller
+  const int tx = threads_for(p.H, VPT), group = STAGES * (static_cast<int>(sizeof(DY)) + (p.dr ? 4 : 2)) * p.H;
+  int groups = kBackThreads / tx;
+  if (groups > (kSlotBytes - 2 * p.H) / group) groups = (kSlotBytes - 2 * p.H) / group;
+  if (groups > kBackGroups) groups = kBackGroups;
+  return launch_pdl(kern, dim3(blocks), dim3(groups * tx), groups * group + 2 * p.H, s, p, tx);
+}
+
+// Two rows ahead where two rows of one group fit in shared memory, one for the
+// widest; narrow rows (one or two vectors per thread) four.
 template <typename DY>
-cudaError_t launch_backward_typed(NormBackwardLaunch p, bool vec, cudaStream_t s) {
+cudaError_t launch_backward_typed(const NormBackwardLaunch& p, bool vec, cudaStream_t s) {
   const int blocks = norm_backward_blocks(p.T);
+  const int row = (static_cast<int>(sizeof(DY)) + (p.dr ? 4 : 2)) * p.H;
   cudaError_t e;
   if (vec && p.H <= 16384) {
-    if (p.H <= 4096)
-      e = launch_pdl(norm_backward_kernel<DY, 1, 4>, dim3(blocks), dim3(threads_for(p.H, 1)), 0, s, p);
-    else if (p.H <= 8192)
-      e = launch_pdl(norm_backward_kernel<DY, 2, 2>, dim3(blocks), dim3(threads_for(p.H, 2)), 0, s, p);
-    else
-      e = launch_pdl(norm_backward_kernel<DY, 4, 1>, dim3(blocks), dim3(threads_for(p.H, 4)), 0, s, p);
+    if (p.H <= 256) e = launch_backward_vec<DY, 1, 4>(p, blocks, s);
+    else if (p.H <= 512) e = launch_backward_vec<DY, 2, 4>(p, blocks, s);
+    else if (2 * row + 2 * p.H <= kSlotBytes) e = launch_backward_vec<DY, 4, 2>(p, blocks, s);
+    else e = launch_backward_vec<DY, 4, 1>(p, blocks, s);
   } else {
     e = launch_pdl(norm_dw_any_kernel<DY>, dim3((p.H + 127) / 128, blocks), dim3(128), 0, s, p);
     if (e == cudaSuccess) e = launch_pdl(norm_dx_any_kernel<DY>, dim3(p.T), dim3(256), 0, s, p);
@@ -441,6 +634,17 @@ cudaError_t launch_rmsnorm(const NormLaunch& p, cudaStream_t s) {
                       reinterpret_cast<uintptr_t>(p.y) | (2 * reinterpret_cast<uintptr_t>(p.q));
   if (p.H % 8 != 0 || a % 16 != 0 || p.H > 32768)
     return launch_pdl(norm_any_kernel, dim3(p.T), dim3(256), 0, s, p);
+  if (p.T >= kManyRowsPerSm * device_sm_count() && p.H <= 4096) {
+    if (p.H <= 1024) {
+      const dim3 grid((p.T + 3) / 4), block(128);
+      if (p.H <= 256) return launch_pdl(norm_warp_kernel<1>, grid, block, 0, s, p);
+      if (p.H <= 512) return launch_pdl(norm_warp_kernel<2>, grid, block, 0, s, p);
+      return launch_pdl(norm_warp_kernel<4>, grid, block, 0, s, p);
+    }
+    if (p.H <= 2048) return launch_pdl(norm_kernel<2>, dim3(p.T), dim3(threads_for(p.H, 2)), 0, s, p);
+    if (p.H <= 2944) return launch_pdl(norm_kernel<3>, dim3(p.T), dim3(threads_for(p.H, 3)), 0, s, p);
+    return launch_pdl(norm_kernel<4>, dim3(p.T), dim3(threads_for(p.H, 4)), 0, s, p);
+  }
   if (p.H <= 2048) return launch_pdl(norm_kernel<1>, dim3(p.T), dim3(threads_for(p.H, 1)), 0, s, p);
   if (p.H <= 8192) return launch_pdl(norm_kernel<2>, dim3(p.T), dim3(threads_for(p.H, 2)), 0, s, p);
   return launch_pdl(norm_kernel<4>, dim3(p.T), dim3(threads_for(p.H, 4)), 0, s, p);
@@ -448,8 +652,8 @@ cudaError_t launch_rmsnorm(const NormLaunch& p, cudaStream_t s) {
 
 // One row of partial weight gradients per block: one block per SM, fewer for few rows.
 int norm_backward_blocks(int32_t T) {
-  const int rows = (T + 3) / 4, sms = device_sm_count();
-  return rows < sms ? (rows > 0 ? rows : 1) : sms;
+  const int most = device_sm_count();
+  return T < most ? (T > 0 ? T : 1) : most;
 }
 
 cudaError_t launch_rmsnorm_backward(const NormBackwardLaunch& p, cudaStream_t s) {

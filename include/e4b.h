@@ -399,7 +399,8 @@ size_t e4b_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H);
  *   r, rstd : the forward's stream [T, H] bf16 and [T] fp32              (device, read)
  *   dx      : [T, H] bf16                                               (device, written)
  *   dweight : [H] fp32 (zeros when T == 0)                              (device, written)
- *   ws      : 256-byte aligned, >= e4b_rmsnorm_backward_workspace_bytes(T, H)
+ *   ws      : 256-byte aligned, >= e4b_rmsnorm_backward_workspace_bytes(T, H);
+ *             its first bytes hold the device status word (e4b_device_status)
  * dx may be the same buffer as dr, r or a bf16 dy; other overlaps are refused.
  */
 e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t* dr, const uint16_t* r,
