@@ -191,16 +191,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == WARP_TMA) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, par = 0;
-      bool ok = true;
-      for (int tile = first; ok && tile < total; tile += step) {
-        int mt, nt;
-        tile_at(p, tile, mt, nt);
-        const int m0 = (mt * CG + rank) * BM, n0 = nt * NT;
-        for (int ks = 0; ks < ksteps; ++ks) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wctx, 1101)) { ok = false; break; }
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, par = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < total; tile += step) {
+      int mt, nt;
+      tile_at(p, tile, mt, nt);
+      const int m0 = (mt * CG + rank) * BM, n0 = nt * NT;
+      for (int ks = 0; ks < ksteps; ++ks) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wctx, 1101)) { ok = false; break; }
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
           const uint32_t bar = CG == 2 ? cluster_addr(&full[stage], 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
@@ -228,19 +228,26 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else {
             load(b, &tm_b, k0, nb);
           }
-          armed |= 1u << stage;
-          par = (par & ~(1u << stage)) | (phase << stage);
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
-      }
-      if (!ok) {   // let every issued copy land before the CTA's shared memory is released
-        for (int s = 0; s < C::STAGES; ++s)      // (rank 1 has no barrier of its own to watch: it waits the limit out)
-          if (armed & (1u << s)) mbar_drain(rank == 0 ? &full[s] : s_never, rank == 0 ? (par >> s) & 1u : 0u, kDrainNs);
+        __syncwarp();
+        armed |= 1u << stage;
+        par = (par & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
       }
     }
+    if (!ok && lane == 0) {   // let every issued copy land before the CTA's shared memory is released
+      for (int s = 0; s < C::STAGES; ++s)        // (rank 1 has no barrier of its own to watch: it waits the limit out)
+        if (armed & (1u << s)) mbar_drain(rank == 0 ? &full[s] : s_never, rank == 0 ? (par >> s) & 1u : 0u, kDrainNs);
+    }
   } else if (warp == WARP_MMA) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(CG * BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      // descriptors differ only in their start address (16-byte units): 16 of K are 32 bytes along a row, or two
+      // 8-row atoms where K is the row
+      const uint32_t base = smem_u32(smem);
+      const uint64_t da0 = A_MN ? smem_desc_mn_sw128(base) : smem_desc_sw128(base);
+      const uint64_t db0 = B_MN ? smem_desc_mn_sw128(base + C::A_BYTES) : smem_desc_sw128(base + C::A_BYTES);
+      constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
@@ -249,35 +256,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int tile = first; ok && tile < total; tile += step, ++it) {
         const int buf = it & 1;
         const uint32_t aphase = (it >> 1) & 1;
-        if (!mbar_wait(&acc_empty[buf], aphase ^ 1u, wctx, 1201)) { ok = false; break; }
+        if (!mbar_wait_warp(&acc_empty[buf], aphase ^ 1u, wctx, 1201)) { ok = false; break; }
         tc_fence_after_sync();
         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
         for (int ks = 0; ks < ksteps; ++ks) {
-          if (!mbar_wait(&full[stage], phase, wctx, 1202)) { ok = false; break; }
-          tc_fence_after_sync();
-          const uint32_t a0 = smem_u32(smem + stage * C::STAGE_BYTES);
-          const uint32_t b0 = a0 + C::A_BYTES;
+          if (!mbar_wait_warp(&full[stage], phase, wctx, 1202)) { ok = false; break; }
+          const uint64_t da = da0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+          const uint64_t db = db0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {          // 16 of K: 32 bytes along a row, or two 8-row atoms
-            const uint64_t da = A_MN ? smem_desc_mn_sw128(a0 + kk * 2048) : smem_desc_sw128(a0 + kk * 32);
-            const uint64_t db = B_MN ? smem_desc_mn_sw128(b0 + kk * 2048) : smem_desc_sw128(b0 + kk * 32);
-            if constexpr (CG == 2) umma_bf16_ss_pair(d, da, db, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
-            else umma_bf16_ss(d, da, db, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              if constexpr (CG == 2) umma_bf16_ss_pair(d, da + kk * a_step, db + kk * b_step, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+              else umma_bf16_ss(d, da + kk * a_step, db + kk * b_step, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+            }
+            if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
+            else umma_commit(&empty[stage]);
+            if (ks == ksteps - 1) {
+              if constexpr (CG == 2) umma_commit_pair(&acc_full[buf]);
+              else umma_commit(&acc_full[buf]);
+            }
           }
-          if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
-          else umma_commit(&empty[stage]);
+          __syncwarp();
           issued = true;
           last_bar = &empty[stage];
           last_par = phase;
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (!ok) break;
-        if constexpr (CG == 2) umma_commit_pair(&acc_full[buf]);
-        else umma_commit(&acc_full[buf]);
-        last_bar = &acc_full[buf];
-        last_par = aphase;
       }
-      if (!ok && issued) mbar_drain(last_bar, last_par, kDrainNs);
+      if (!ok && issued && lane == 0) mbar_drain(last_bar, last_par, kDrainNs);   // MMAs in flight finish first
     }
   } else if (warp >= WARP_EPI0) {
     const int q = warp & 3;                        // TMEM lanes 32q..32q+31: D row = lane

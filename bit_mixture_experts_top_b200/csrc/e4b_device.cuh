@@ -137,6 +137,24 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// mbar_wait by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w, int32_t where) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, w, where));
+}
+
+// True in one lane of the (converged) warp.  A loop that the whole warp runs, with the issue of an asynchronous
+// instruction under elect_one(), keeps its operands in uniform registers; the same loop run by one lane alone
+// moves every descriptor there for each instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
