@@ -651,7 +651,7 @@ static FfnLayout ffn_layout(const e4b_ffn_desc& d, int32_t T) {
   L.forward_total = o;
   L.g = take(t * 2 * I * 4);
   L.dG = take(t * 2 * I * 2);
-  L.gu_sums = take((t + 31) / 32 * 2 * I * 4);
+  L.gu_sums = take(dense_colsum_rows(T) * 2 * I * 4);
   L.dn_sums = take(static_cast<size_t>(column_sum_bf16_blocks(T)) * d.H * 4);
   L.total = o;
   return L;
@@ -728,6 +728,7 @@ static e4b_status run_ffn(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, c
   dn.add = add;
   dn.out = out;
   dn.status = status;
+  dn.b_early = 1;
   return launch_dense_gemm(dn, s);
 }
 
@@ -784,6 +785,7 @@ e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x,
   base.beta = d->glu_beta;
   base.status = at<int32_t>(ws, L.status);
   e4b_status st = E4B_OK;
+  int32_t sum_rows = 0;
   if (dx || dw_gu || dgu_bias) {                     // dG = act'(G) applied to dout W_dn
     DenseGemmLaunch g = base;
     g.epi = kEpiDact;
@@ -796,6 +798,7 @@ e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x,
     g.out = dG;
     g.g_in = at<float>(ws, L.g);
     g.colsum = dgu_bias ? at<float>(ws, L.gu_sums) : nullptr;
+    g.colsum_rows = &sum_rows;
     st = launch_dense_gemm(g, s);
     if (st != E4B_OK) return st;
   }
@@ -809,6 +812,7 @@ e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x,
     g.b = w_gu;
     g.b_mn = true;
     g.out = dx;
+    g.b_early = 1;
     st = launch_dense_gemm(g, s);
     if (st != E4B_OK) return st;
   }
@@ -834,7 +838,7 @@ e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x,
     st = launch_dense_gemm(g, s);
     if (st != E4B_OK) return st;
   }
-  if (dgu_bias && launch_column_sum(at<float>(ws, L.gu_sums), (T + 31) / 32, 2 * d->I, dgu_bias, s) != cudaSuccess)
+  if (dgu_bias && launch_column_sum(at<float>(ws, L.gu_sums), sum_rows, 2 * d->I, dgu_bias, s) != cudaSuccess)
     return E4B_ERR_CUDA;
   if (ddn_bias && launch_column_sum_bf16(dout, T, d->H, at<float>(ws, L.dn_sums), ddn_bias, s) != cudaSuccess)
     return E4B_ERR_CUDA;

@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "e4b_device.cuh"
@@ -59,13 +60,15 @@ struct Params {
   int32_t act;
   float alpha, limit, beta;
   const float* bias;        // gate_up: [2I]; linear: [N]; or null
+  int32_t bias_words;       // bias is 16-byte aligned
   const uint16_t* add;      // linear: [M, N] bf16 or null
   uint16_t* out;            // bf16: h [M, I], D [M, N] or dG [M, 2I]
   float* g_out;             // gate_up: G [M, 2I] fp32 or null
   const float* g_in;        // dact: G [M, 2I]
-  float* colsum;            // dact: [ceil(M / 32), 2I] column sums of dG per 32 rows, or null
+  float* colsum;            // dact: partial column sums of dG, [rows, 2I] (one per 32 rows, or per split CTA), or null
   int32_t* status;
   int32_t clear_status;     // this launch is the first of its call: block 0 clears the status words
+  int32_t b_early;          // split: the launch before this one does not write B
   uint64_t wait_limit_ns;
 };
 
@@ -116,23 +119,121 @@ __device__ __forceinline__ void act_grads(const Params& p, float gate, float up,
   du = gate * s;
 }
 
-// Sums 16 values per lane over the warp by halving: each step a lane keeps half
-// of its columns and hands over the rest, 16 shuffles in all.  Lane l ends with
-// the sum of column (l >> 1) with its bits reversed in the order kept below.
-__device__ __forceinline__ float warp_column_sum16(float (&v)[16], int lane, int& col) {
+// Sums 8 values per lane over the warp by halving: in three steps a lane keeps
+// half of its columns and hands over the rest, then two plain steps; 9 shuffles.
+// Lanes 4j hold the sum of one column each, `col`.
+__device__ __forceinline__ float warp_column_sum8(const float (&in)[8], int lane, int& col) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = in[i];
   col = 0;
 #pragma unroll
-  for (int h = 8; h >= 1; h >>= 1) {
-    const bool upper = lane & (2 * h);
+  for (int h = 4; h >= 1; h >>= 1) {
+    const bool upper = lane & (4 * h);
 #pragma unroll
     for (int i = 0; i < h; ++i) {
       const float keep = upper ? v[i + h] : v[i];
       const float give = upper ? v[i] : v[i + h];
-      v[i] = keep + __shfl_xor_sync(kFull, give, 2 * h);
+      v[i] = keep + __shfl_xor_sync(kFull, give, 4 * h);
     }
     col += upper ? h : 0;
   }
-  return v[0] + __shfl_xor_sync(kFull, v[0], 1);
+  const float s = v[0] + __shfl_xor_sync(kFull, v[0], 2);
+  return s + __shfl_xor_sync(kFull, s, 1);
+}
+
+__device__ __forceinline__ void add_bias8(const Params& p, int at, float (&f)[8]) {
+  if (!p.bias) return;
+  if (p.bias_words) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + at));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + at) + 1);
+    f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+    f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += __ldg(p.bias + at + i);
+  }
+}
+
+__device__ __forceinline__ void store8f(float* o, const float (&f)[8]) {
+  reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// The epilogues, eight adjacent columns of one row at a time (fp32 sums in, `col` a multiple of 8, below N).
+__device__ __forceinline__ void finish_gate_up(const Params& p, int row, bool row_in, int col, float (&g)[8],
+                                               float (&u)[8]) {
+  add_bias8(p, col, g);
+  add_bias8(p, p.N + col, u);
+  if (!row_in) return;
+  if (p.g_out) {
+    float* o = p.g_out + static_cast<int64_t>(row) * 2 * p.N + col;
+    store8f(o, g);
+    store8f(o + p.N, u);
+  }
+  const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = expert_act(ep, g[i], u[i]);
+  store8(p.out + static_cast<int64_t>(row) * p.N + col, g);
+}
+
+__device__ __forceinline__ void finish_linear(const Params& p, int row, bool row_in, int col, float (&f)[8]) {
+  add_bias8(p, col, f);
+  if (!row_in) return;
+  const int64_t at = static_cast<int64_t>(row) * p.N + col;
+  if (p.add) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p.add + at);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] += __uint_as_float(w[i] << 16);
+      f[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  store8(p.out + at, f);
+}
+
+// All lanes of the warp call it with rows row0 + lane (row0 a multiple of 32).
+__device__ __forceinline__ void finish_dact(const Params& p, int row, bool row_in, int col, int lane,
+                                            const float (&dh)[8]) {
+  float dg[8], du[8];
+#pragma unroll
+  for (int j = 0; j < 8; j += 4) {
+    float4 fg = make_float4(0.f, 0.f, 0.f, 0.f), fu = fg;
+    if (row_in) {
+      const float* gp = p.g_in + static_cast<int64_t>(row) * 2 * p.N + col + j;
+      fg = *reinterpret_cast<const float4*>(gp);
+      fu = *reinterpret_cast<const float4*>(gp + p.N);
+    }
+    const float gv[4] = {fg.x, fg.y, fg.z, fg.w}, uv[4] = {fu.x, fu.y, fu.z, fu.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      act_grads(p, gv[i], uv[i], dg[j + i], du[j + i]);
+      dg[j + i] = row_in ? dg[j + i] * dh[j + i] : 0.0f;
+      du[j + i] = row_in ? du[j + i] * dh[j + i] : 0.0f;
+    }
+  }
+  if (row_in) {
+    uint16_t* o = p.out + static_cast<int64_t>(row) * 2 * p.N + col;
+    store8(o, dg);
+    store8(o + p.N, du);
+  }
+  if (p.colsum) {                         // from the fp32 values, before their rounding to bf16
+    const int row0 = row - lane;
+    int c;
+    const float sg = warp_column_sum8(dg, lane, c);
+    const float su = warp_column_sum8(du, lane, c);
+    if ((lane & 3) == 0 && row0 < p.M) {
+      float* o = p.colsum + static_cast<int64_t>(row0 / 32) * 2 * p.N + col + c;
+      o[0] = sg;
+      o[p.N] = su;
+    }
+  }
+}
+
+__device__ __forceinline__ void take8(const uint32_t (&r)[16], int j, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[j + i]);
 }
 
 template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
@@ -304,98 +405,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int c0 = half * (NT / 2); c0 < (half + 1) * (NT / 2); c0 += 16) {
         const int col = nt * NT + c0;
         if (col >= p.N) break;
-        if constexpr (EPI == kEpiGateUp) {
-          uint32_t g[16], u[16];
-          tmem_ld_32x32b_x16(taddr + c0, g);
-          tmem_ld_32x32b_x16(taddr + NT + c0, u);
-          tmem_ld_wait();
-          const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
+        uint32_t r[16], u[16];
+        tmem_ld_32x32b_x16(taddr + c0, r);
+        if constexpr (EPI == kEpiGateUp) tmem_ld_32x32b_x16(taddr + NT + c0, u);
+        tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            if (col + j >= p.N) break;
-            float fg[8], fu[8], h[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              fg[i] = __uint_as_float(g[j + i]) + (p.bias ? __ldg(p.bias + col + j + i) : 0.0f);
-              fu[i] = __uint_as_float(u[j + i]) + (p.bias ? __ldg(p.bias + p.N + col + j + i) : 0.0f);
-              h[i] = expert_act(ep, fg[i], fu[i]);
-            }
-            if (row_in) {
-              store8(p.out + static_cast<int64_t>(row) * p.N + col + j, h);
-              if (p.g_out) {
-                float4* go = reinterpret_cast<float4*>(p.g_out + static_cast<int64_t>(row) * 2 * p.N + col + j);
-                go[0] = make_float4(fg[0], fg[1], fg[2], fg[3]);
-                go[1] = make_float4(fg[4], fg[5], fg[6], fg[7]);
-                go = reinterpret_cast<float4*>(p.g_out + static_cast<int64_t>(row) * 2 * p.N + p.N + col + j);
-                go[0] = make_float4(fu[0], fu[1], fu[2], fu[3]);
-                go[1] = make_float4(fu[4], fu[5], fu[6], fu[7]);
-              }
-            }
-          }
-        } else if constexpr (EPI == kEpiLinear) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(taddr + c0, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            if (col + j >= p.N) break;
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              f[i] = __uint_as_float(r[j + i]) + (p.bias ? __ldg(p.bias + col + j + i) : 0.0f);
-            if (row_in) {
-              const int64_t at = static_cast<int64_t>(row) * p.N + col + j;
-              if (p.add) {
-                const uint4 a = *reinterpret_cast<const uint4*>(p.add + at);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  f[2 * i] += __uint_as_float(w[i] << 16);
-                  f[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
-                }
-              }
-              store8(p.out + at, f);
-            }
-          }
-        } else {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(taddr + c0, r);
-          tmem_ld_wait();
-          float dg[16], du[16];
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            float4 fg = make_float4(0.f, 0.f, 0.f, 0.f), fu = fg;
-            if (row_in && col + j < p.N) {
-              const float* gp = p.g_in + static_cast<int64_t>(row) * 2 * p.N + col + j;
-              fg = *reinterpret_cast<const float4*>(gp);
-              fu = *reinterpret_cast<const float4*>(gp + p.N);
-            }
-            const float gv[4] = {fg.x, fg.y, fg.z, fg.w}, uv[4] = {fu.x, fu.y, fu.z, fu.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              act_grads(p, gv[i], uv[i], dg[j + i], du[j + i]);
-              const float dh = __uint_as_float(r[j + i]);          // 0 in rows past M
-              dg[j + i] = row_in ? dg[j + i] * dh : 0.0f;
-              du[j + i] = row_in ? du[j + i] * dh : 0.0f;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            if (row_in && col + j < p.N) {
-              uint16_t* o = p.out + static_cast<int64_t>(row) * 2 * p.N + col + j;
-              store8(o, dg + j);
-              store8(o + p.N, du + j);
-            }
-          }
-          if (p.colsum) {                         // from the fp32 values, before their rounding to bf16
-            float* o = p.colsum + static_cast<int64_t>(row0 / 32) * 2 * p.N;
-            int c;
-            const float sg = warp_column_sum16(dg, lane, c);
-            const float su = warp_column_sum16(du, lane, c);
-            if ((lane & 1) == 0 && col + c < p.N && row0 < p.M) {
-              o[col + c] = sg;
-              o[p.N + col + c] = su;
-            }
+        for (int j = 0; j < 16; j += 8) {
+          if (col + j >= p.N) break;
+          float f[8];
+          take8(r, j, f);
+          if constexpr (EPI == kEpiGateUp) {
+            float fu[8];
+            take8(u, j, fu);
+            finish_gate_up(p, row, row_in, col + j, f, fu);
+          } else if constexpr (EPI == kEpiLinear) {
+            finish_linear(p, row, row_in, col + j, f);
+          } else {
+            finish_dact(p, row, row_in, col + j, lane, f);
           }
         }
       }
@@ -418,43 +444,321 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// ---------------------------------------------------------------------- split along K
+
+// A product too small to give every SM a tile: a cluster of S CTAs shares one
+// 128 x 128 tile, each multiplies its part of K, and the partial tiles meet
+// through distributed shared memory: every CTA adds the S parts, in rank order,
+// of its share of the rows (whole rows, a warp each: contiguous 512-byte reads
+// from every rank and contiguous stores; a lane-per-row layout took five times
+// as long) and runs the epilogue on them.  Stages hold 128 of K: with tiles this
+// narrow the per-stage wait, not the MMA, is what costs.
+//
+// B (weights) may be loaded before the previous launch has completed when that
+// launch does not write it (b_early): the first stages then hide its tail.
+struct SplitCfg {
+  static constexpr int BN = 128, SK = 128;
+  static constexpr int A_BYTES = BM * SK * 2, B_BYTES = BN * SK * 2, ATOM = BM * BK * 2;   // an atom: 64 of K
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 3;
+  static constexpr int PITCH = BN + 4;                        // floats per row of the partial tile (conflict-free)
+  static constexpr int OFF_SUMS = BM * PITCH * 4;             // dact: column sums per warp, behind the partial tile
+  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 1) * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static_assert(OFF_SUMS + EPI_WARPS * 2 * BN * 4 <= STAGES * STAGE_BYTES, "both reuse the stages");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 bias4(const Params& p, int at) {
+  if (p.bias_words) return __ldg(reinterpret_cast<const float4*>(p.bias + at));
+  return make_float4(__ldg(p.bias + at), __ldg(p.bias + at + 1), __ldg(p.bias + at + 2), __ldg(p.bias + at + 3));
+}
+
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+}
+
+__device__ __forceinline__ uint2 pack4(const float4& v) { return make_uint2(pack2(v.x, v.y), pack2(v.z, v.w)); }
+
+template <bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(THREADS, 1)
+    dense_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                       const Params p, int S) {
+  using C = SplitCfg;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  int32_t* s_abort = reinterpret_cast<int32_t*>(smem + C::OFF_MISC + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == WARP_MMA) {      // (no other tensor-memory kernel of the library leaves room for this one on its SM)
+    tmem_alloc(s_tmem, C::BN);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *s_tmem;
+  const WaitCtx wctx{s_abort, p.status, p.wait_limit_ns};
+  constexpr int NT = EPI == kEpiGateUp ? C::BN / 2 : C::BN;
+  int mt, nt;
+  tile_at(p, blockIdx.x / S, mt, nt);
+  const int m0 = mt * BM, n0 = nt * NT;
+  const int steps = (p.K + C::SK - 1) / C::SK;
+  const int first = static_cast<int>(static_cast<int64_t>(steps) * rank / S);
+  const int last = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / S);      // S <= steps: never empty
+  auto atoms_of = [&](int ks) { return min(2, (p.K - ks * C::SK + BK - 1) / BK); };
+
+  if (warp == WARP_TMA) {
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, par = 0;
+    bool ok = true;
+    auto load_a = [&](int ks, int stage) {
+      uint8_t* a = smem + stage * C::STAGE_BYTES;
+      for (int i = 0; i < atoms_of(ks); ++i, a += C::ATOM) {
+        const int k0 = ks * C::SK + i * BK;
+        if constexpr (A_MN) {
+          tma_load_2d(a, &tm_a, &full[stage], m0, k0);
+          tma_load_2d(a + 8192, &tm_a, &full[stage], m0 + 64, k0);
+        } else {
+          tma_load_2d(a, &tm_a, &full[stage], k0, m0);
+        }
+      }
+    };
+    auto load_b = [&](int ks, int stage) {
+      uint8_t* b = smem + stage * C::STAGE_BYTES + C::A_BYTES;
+      mbar_arrive_expect_tx(&full[stage], atoms_of(ks) * 2 * C::ATOM);
+      for (int i = 0; i < atoms_of(ks); ++i, b += C::ATOM) {
+        const int k0 = ks * C::SK + i * BK;
+        if constexpr (EPI == kEpiGateUp) {
+          tma_load_2d(b, &tm_b, &full[stage], k0, n0);
+          tma_load_2d(b + 8192, &tm_b, &full[stage], k0, p.N + n0);
+        } else if constexpr (B_MN) {
+          tma_load_2d(b, &tm_b, &full[stage], n0, k0);
+          tma_load_2d(b + 8192, &tm_b, &full[stage], n0 + 64, k0);
+        } else {
+          tma_load_2d(b, &tm_b, &full[stage], k0, n0);
+        }
+      }
+    };
+    const int early = p.b_early ? min(C::STAGES, last - first) : 0;
+    if (elect_one())
+      for (int i = 0; i < early; ++i) load_b(first + i, i);
+    __syncwarp();
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int ks = first; ks < last; ++ks) {
+      if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wctx, 1501)) { ok = false; break; }
+      if (elect_one()) {
+        if (ks - first >= early) load_b(ks, stage);
+        load_a(ks, stage);
+      }
+      __syncwarp();
+      armed |= 1u << stage;
+      par = (par & ~(1u << stage)) | (phase << stage);
+      if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+    }
+    if (!ok && lane == 0) {
+      for (int s = 0; s < C::STAGES; ++s)
+        if (armed & (1u << s)) mbar_drain(&full[s], (par >> s) & 1u, kDrainNs);
+    }
+  } else if (warp == WARP_MMA) {
+    constexpr uint32_t idesc = idesc_bf16_f32(BM, C::BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+    const uint32_t base = smem_u32(smem);
+    const uint64_t da0 = A_MN ? smem_desc_mn_sw128(base) : smem_desc_sw128(base);
+    const uint64_t db0 = B_MN ? smem_desc_mn_sw128(base + C::A_BYTES) : smem_desc_sw128(base + C::A_BYTES);
+    constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    pdl_wait();
+    if (p.clear_status && blockIdx.x == 0 && lane < 2) p.status[lane] = 0;
+    for (int ks = first; ks < last; ++ks) {
+      if (!mbar_wait_warp(&full[stage], phase, wctx, 1502)) { ok = false; break; }
+      const int atoms = atoms_of(ks);
+      const uint64_t da = da0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+      const uint64_t db = db0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < C::SK / 16; ++kk) {
+          if (kk >= 4 * atoms) break;
+          const uint32_t off = (kk >> 2) * (C::ATOM >> 4);
+          umma_bf16_ss(tmem_base, da + off + (kk & 3) * a_step, db + off + (kk & 3) * b_step, idesc,
+                       (ks > first || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(&empty[stage]);
+        if (ks == last - 1) umma_commit(acc_full);
+      }
+      __syncwarp();
+      issued = true;
+      if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+    }
+    if (!ok && issued && lane == 0)
+      mbar_drain(&empty[stage == 0 ? C::STAGES - 1 : stage - 1], stage == 0 ? phase ^ 1u : phase, kDrainNs);
+  } else if (warp >= WARP_EPI0) {
+    // this CTA's partial tile into its shared memory (every stage has been consumed by then)
+    const int q = warp & 3, half = (warp - WARP_EPI0) >> 2;
+    pdl_wait();
+    if (__all_sync(kFull, mbar_wait_sleep(acc_full, 0, wctx, 1503, 64))) {
+      tc_fence_after_sync();
+      float* row = reinterpret_cast<float*>(smem) + (32 * q + lane) * C::PITCH;
+      if (m0 + 32 * q < p.M) {
+#pragma unroll
+        for (int c0 = half * (C::BN / 2); c0 < (half + 1) * (C::BN / 2); c0 += 32) {
+          uint32_t r[16], u[16];
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0 + 16, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            *reinterpret_cast<uint4*>(row + c0 + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+            *reinterpret_cast<uint4*>(row + c0 + 16 + j) = make_uint4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+          }
+        }
+      }
+      tc_fence_before_sync();
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp >= WARP_EPI0) {
+    const int ew = warp - WARP_EPI0;
+    const int rows = min(BM, p.M - m0);
+    const uint32_t mine = smem_u32(smem) + 16 * lane;
+    // rows go round the ranks, then round the warps; a lane holds four adjacent columns of the tile
+    const int tile_col = 4 * lane;
+    const int col = n0 + (EPI == kEpiGateUp ? tile_col & (NT - 1) : tile_col);
+    const bool col_in = col < p.N;
+    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (EPI != kEpiDact && p.bias && col_in) bias = bias4(p, EPI == kEpiGateUp && lane >= 16 ? p.N + col : col);
+    float4 sg = make_float4(0.f, 0.f, 0.f, 0.f), su = sg;      // dact: column sums over this warp's rows
+#pragma unroll 2
+    for (int r = rank + S * ew; r < rows; r += S * EPI_WARPS) {
+      const int64_t row = m0 + r;
+      float4 f = bias;
+#pragma unroll 4
+      for (int s = 0; s < S; ++s) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine + r * C::PITCH * 4), "r"(s));
+        add4(f, load_cluster(at));
+      }
+      if constexpr (EPI == kEpiGateUp) {               // lanes 0..15 hold gate, 16..31 the matching up features
+        if (p.g_out && col_in)
+          *reinterpret_cast<float4*>(p.g_out + row * 2 * p.N + (lane >= 16 ? p.N : 0) + col) = f;
+        float4 u;
+        u.x = __shfl_down_sync(kFull, f.x, 16);
+        u.y = __shfl_down_sync(kFull, f.y, 16);
+        u.z = __shfl_down_sync(kFull, f.z, 16);
+        u.w = __shfl_down_sync(kFull, f.w, 16);
+        if (lane < 16 && col_in) {
+          const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
+          f.x = expert_act(ep, f.x, u.x);
+          f.y = expert_act(ep, f.y, u.y);
+          f.z = expert_act(ep, f.z, u.z);
+          f.w = expert_act(ep, f.w, u.w);
+          *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
+        }
+      } else if constexpr (EPI == kEpiLinear) {
+        if (col_in) {
+          if (p.add) {
+            const uint2 a = *reinterpret_cast<const uint2*>(p.add + row * p.N + col);
+            add4(f, make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u),
+                                __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xFFFF0000u)));
+          }
+          *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
+        }
+      } else if (col_in) {
+        const float* gp = p.g_in + row * 2 * p.N + col;
+        const float4 g = *reinterpret_cast<const float4*>(gp), u = *reinterpret_cast<const float4*>(gp + p.N);
+        float4 dg, du;
+        act_grads(p, g.x, u.x, dg.x, du.x);
+        act_grads(p, g.y, u.y, dg.y, du.y);
+        act_grads(p, g.z, u.z, dg.z, du.z);
+        act_grads(p, g.w, u.w, dg.w, du.w);
+        dg = make_float4(dg.x * f.x, dg.y * f.y, dg.z * f.z, dg.w * f.w);
+        du = make_float4(du.x * f.x, du.y * f.y, du.z * f.z, du.w * f.w);
+        *reinterpret_cast<uint2*>(p.out + row * 2 * p.N + col) = pack4(dg);
+        *reinterpret_cast<uint2*>(p.out + row * 2 * p.N + p.N + col) = pack4(du);
+        add4(sg, dg);
+        add4(su, du);
+      }
+    }
+    if constexpr (EPI == kEpiDact) {
+      if (p.colsum) {                                  // the warps' sums, one row of partial sums per CTA
+        float4* sums = reinterpret_cast<float4*>(smem + C::OFF_SUMS);
+        sums[ew * 64 + lane] = sg;
+        sums[ew * 64 + 32 + lane] = su;
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+        const int i = threadIdx.x - 32 * WARP_EPI0;
+        if (i < 64) {
+          float4 t = sums[i];
+          for (int w = 1; w < EPI_WARPS; ++w) add4(t, sums[w * 64 + i]);
+          const int c = n0 + 4 * (i & 31);
+          if (c < p.N)
+            *reinterpret_cast<float4*>(p.colsum + (static_cast<int64_t>(mt) * S + rank) * 2 * p.N + (i >> 5) * p.N + c) = t;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();                                 // the partial tile stays until every rank has read it
+  if (warp == WARP_MMA) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, C::BN);
+  }
+}
+
 // ---------------------------------------------------------------------- host side
 
-template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
-e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
-  using C = Cfg<BN, CG>;
-  auto kern = dense_gemm_kernel<BN, CG, A_MN, B_MN, EPI>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  });
-  if (attr_err != cudaSuccess) return E4B_ERR_CUDA;
-  constexpr int NT = EPI == kEpiGateUp ? BN / 2 : BN;
+// Tensor maps of both operands.  K-contiguous: [rows, K], boxes of 64 K x tile rows; M/N-contiguous:
+// [K, rows], boxes of 64 rows x 64 K.
+template <bool A_MN, bool B_MN, int EPI>
+bool encode_operands(const DenseGemmLaunch& g, int b_box, CUtensorMap* ta, CUtensorMap* tb) {
   const uint64_t b_rows = EPI == kEpiGateUp ? 2 * static_cast<uint64_t>(g.N) : g.N;
-  CUtensorMap ta, tb;
-  // K-contiguous: [rows, K], boxes of 64 K x tile rows; M/N-contiguous: [K, rows], boxes of 64 rows x 64 K
-  const bool ok_a = A_MN ? encode_tma_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, g.M, g.K,
-                                         static_cast<uint64_t>(g.M) * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)
-                         : encode_tma_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, g.K, g.M,
-                                         static_cast<uint64_t>(g.K) * 2, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B);
-  const bool ok_b = B_MN ? encode_tma_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.b, b_rows, g.K, b_rows * 2, 64, BK,
-                                         CU_TENSOR_MAP_SWIZZLE_128B)
-                         : encode_tma_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.b, g.K, b_rows,
-                                         static_cast<uint64_t>(g.K) * 2, BK, EPI == kEpiGateUp ? NT : C::B_ROWS,
-                                         CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!ok_a || !ok_b) return E4B_ERR_CUDA;
+  auto enc = [](CUtensorMap* m, const uint16_t* p, uint64_t rows, uint64_t K, bool mn, int box) {
+    return mn ? encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rows, K, rows * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)
+              : encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, K, rows, K * 2, BK, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  return enc(ta, g.a, g.M, g.K, A_MN, BM) && enc(tb, g.b, b_rows, g.K, B_MN, b_box);
+}
+
+Params make_params(const DenseGemmLaunch& g, int tile_rows, int tile_cols) {
   Params p;
   p.M = g.M;
   p.N = g.N;
   p.K = g.K;
-  p.m_tiles = (g.M + CG * BM - 1) / (CG * BM);
-  p.n_tiles = (g.N + NT - 1) / NT;
+  p.m_tiles = (g.M + tile_rows - 1) / tile_rows;
+  p.n_tiles = (g.N + tile_cols - 1) / tile_cols;
   p.act = g.act;
   p.alpha = g.alpha;
   p.limit = g.limit;
   p.beta = g.beta;
   p.bias = g.bias;
+  p.bias_words = aligned(g.bias, 16) ? 1 : 0;
   p.add = g.add;
   p.out = g.out;
   p.g_out = g.g_out;
@@ -462,7 +766,28 @@ e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
   p.colsum = g.colsum;
   p.status = g.status;
   p.clear_status = g.clear_status;
+  p.b_early = g.b_early;
   p.wait_limit_ns = kWaitLimitNs;
+  return p;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::once_flag& once, cudaError_t& err) {
+  std::call_once(once, [&] { err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  return err;
+}
+
+template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
+e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
+  using C = Cfg<BN, CG>;
+  auto kern = dense_gemm_kernel<BN, CG, A_MN, B_MN, EPI>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  if (allow_smem(kern, C::SMEM_BYTES, once, attr_err) != cudaSuccess) return E4B_ERR_CUDA;
+  constexpr int NT = EPI == kEpiGateUp ? BN / 2 : BN;
+  CUtensorMap ta, tb;
+  if (!encode_operands<A_MN, B_MN, EPI>(g, EPI == kEpiGateUp ? NT : C::B_ROWS, &ta, &tb)) return E4B_ERR_CUDA;
+  const Params p = make_params(g, CG * BM, NT);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   const int64_t slots = device_sm_count() / CG;
   const dim3 grid(static_cast<unsigned>(CG * (tiles < slots ? tiles : slots)));
@@ -471,18 +796,76 @@ e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
   return e == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
 
-// Pairs where every pair of SMs gets a 256 x 256 tile; else the widest single-CTA tile that
-// still gives every SM one: narrower ones spread a small product.
+// Clusters of S split CTAs that fit the device at once (a GPC's SMs are not a multiple of every S); 0: refused.
+template <bool A_MN, bool B_MN, int EPI>
+int split_slots(int S) {
+  using C = SplitCfg;
+  auto kern = dense_split_kernel<A_MN, B_MN, EPI>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  if (allow_smem(kern, C::SMEM_BYTES, once, attr_err) != cudaSuccess) return 0;
+  static std::atomic<int> cache[16][9];                 // + 1, so that 0 is "not asked yet"
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
+  int n = cache[dev][S].load();
+  if (n > 0) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(S));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 0) n = 0;
+  cache[dev][S].store(n + 1);
+  return n;
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
+  constexpr int NT = EPI == kEpiGateUp ? SplitCfg::BN / 2 : SplitCfg::BN;
+  CUtensorMap ta, tb;
+  if (!encode_operands<A_MN, B_MN, EPI>(g, NT, &ta, &tb)) return E4B_ERR_CUDA;
+  const Params p = make_params(g, BM, NT);
+  if (g.colsum_rows) *g.colsum_rows = p.m_tiles * S;
+  const dim3 grid(static_cast<unsigned>(p.m_tiles * p.n_tiles * S));
+  return launch_pdl_cluster(static_cast<unsigned>(S), dense_split_kernel<A_MN, B_MN, EPI>, grid, dim3(THREADS),
+                            SplitCfg::SMEM_BYTES, s, ta, tb, p, S) == cudaSuccess
+             ? E4B_OK
+             : E4B_ERR_CUDA;
+}
+
+// Which kernel: estimated time in units of one 64-K step of a 256 x 256 pair
+// tile (0.28 us on a B200).  A step of a 128 x 128 tile of one CTA costs 0.8 of
+// that (issue-bound, whatever its width), a 128-K step of the split kernel 1.7
+// (it waits for its loads) and its exchange about 6.
 template <bool A_MN, bool B_MN, int EPI>
 e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
-  const int64_t mt = (g.M + BM - 1) / BM, sms = device_sm_count();
-  auto tiles = [&](int bn) {
-    const int nt = EPI == kEpiGateUp ? bn / 2 : bn;
-    return mt * ((g.N + nt - 1) / nt);
+  const int64_t sms = device_sm_count();
+  auto tiles = [&](int rows, int cols) {
+    const int nt = EPI == kEpiGateUp ? cols / 2 : cols;
+    return (static_cast<int64_t>(g.M) + rows - 1) / rows * ((g.N + nt - 1) / nt);
   };
-  if ((mt + 1) / 2 * (tiles(256) / mt) >= sms / 2) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, s);
-  if (tiles(128) >= sms) return launch_typed<128, 1, A_MN, B_MN, EPI>(g, s);
-  return launch_typed<64, 1, A_MN, B_MN, EPI>(g, s);
+  auto waves = [](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
+  const int64_t k64 = (g.K + BK - 1) / BK, k128 = (g.K + 127) / 128, t128 = tiles(128, 128);
+  const double pair = waves(tiles(256, 256), sms / 2) * k64 + 4.0;
+  const double single = waves(t128, sms) * k64 * 0.8;
+  double best = pair < single ? pair : single;
+  int S = 1;
+  for (int n = 2; n <= 8 && n <= k128 && t128 * n <= sms; ++n) {
+    const double t = static_cast<double>((k128 + n - 1) / n) * 1.7 + 6.0;
+    if (t < best && t128 <= split_slots<A_MN, B_MN, EPI>(n)) {
+      best = t;
+      S = n;
+    }
+  }
+  if (S > 1) return launch_split<A_MN, B_MN, EPI>(g, S, s);
+  if (g.colsum_rows) *g.colsum_rows = (g.M + 31) / 32;
+  if (pair < single) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, s);
+  return launch_typed<128, 1, A_MN, B_MN, EPI>(g, s);
 }
 
 }  // namespace

@@ -239,10 +239,13 @@ struct DenseGemmLaunch {
   uint16_t* out;              // gate_up: h [M, I]; linear: [M, N]; dact: dG [M, 2I]
   float* g_out;               // gate_up: G [M, 2I] or null
   const float* g_in;          // dact: G [M, 2I]
-  float* colsum;              // dact: [ceil(M / 32), 2I] or null
+  float* colsum;              // dact: partial column sums, at most [dense_colsum_rows(M), 2I], or null
+  int32_t* colsum_rows;       // host: how many rows of them the launch writes
   int32_t* status;
   int32_t clear_status;
+  int32_t b_early;            // the previous launch on the stream is the library's own and does not write b
 };
+inline size_t dense_colsum_rows(int32_t M) { return (static_cast<size_t>(M) + 127) / 128 * 8; }
 e4b_status launch_dense_gemm(const DenseGemmLaunch& g, cudaStream_t s);
 
 // The same products for at most kDecodeTokens tokens, bound by the weight stream.  The down launch (gate_up false)
