@@ -691,7 +691,7 @@ static e4b_status run_ffn(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, c
   uint16_t* h = at<uint16_t>(ws, L.h);
   float* g = train ? at<float>(ws, L.g) : nullptr;
   int32_t* status = at<int32_t>(ws, L.status);
-  if (T <= kDecodeTokens) {
+  if (dense_decode_takes(T, d->H, d->I)) {
     const Epilogue ep{nullptr, d->act, d->glu_alpha, d->glu_limit, d->glu_beta};
     const DenseDecodeLaunch gu{T, d->I, d->H, x, w_gu, gu_bias, nullptr, h, g, ep, status};
     const DenseDecodeLaunch dn{T, d->H, d->I, h, w_dn, dn_bias, add, out, nullptr, ep, status};

@@ -248,9 +248,9 @@ struct DenseGemmLaunch {
 inline size_t dense_colsum_rows(int32_t M) { return (static_cast<size_t>(M) + 127) / 128 * 8; }
 e4b_status launch_dense_gemm(const DenseGemmLaunch& g, cudaStream_t s);
 
-// The same products for at most kDecodeTokens tokens, bound by the weight stream.  The down launch (gate_up false)
-// has to follow the gate_up launch that writes its x directly on the stream.
-constexpr int kDecodeTokens = 16;
+// The same products for at most 32 tokens, bound by the weight stream (dense_decode_takes says for which).  The down
+// launch (gate_up false) has to follow the gate_up launch that writes its x directly on the stream.
+bool dense_decode_takes(int32_t T, int32_t H, int32_t I);
 struct DenseDecodeLaunch {
   int32_t T, N, K;            // gate_up: N = I, w = [2I, K]; down: w = [N, K]
   const uint16_t *x, *w;

@@ -438,8 +438,8 @@ size_t e4b_ffn_train_workspace_bytes(const e4b_ffn_desc* d, int32_t T);
  *   out     : [T, H] bf16; may be the same buffer as add      (device, written)
  *   ws      : 256-byte aligned, >= the workspace query; its first bytes hold
  *             the device status word (e4b_device_status)
- * bf16 tensors are 16-byte aligned, fp32 ones 4-byte.  Up to 16 tokens run on
- * the weight-streaming kernel, more on the tcgen05 tiles.
+ * bf16 tensors are 16-byte aligned, fp32 ones 4-byte.  Up to 16 tokens (32 for
+ * small weights) run on the weight-streaming kernel, more on the tcgen05 tiles.
  */
 e4b_status e4b_ffn_forward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x, const uint16_t* w_gu,
                            const uint16_t* w_dn, const float* gu_bias, const float* dn_bias, const uint16_t* add,
