@@ -16,9 +16,10 @@
 // of K where a single CTA with the same width loads 48 KB.  No multicast.
 //
 // One persistent CTA per SM.  Warp 0 issues the TMA loads, warp 1 owns tensor
-// memory and issues the MMAs (M = 128 rows, N = BN columns, two accumulators),
-// warps 4-11 run the epilogue of one tile while the next is multiplied.  Every
-// wait is bounded (E4B_ERR_TIMEOUT in the status word).
+// memory and issues the MMAs (M = 128 rows per CTA, two accumulators), warps
+// 4-19 run the epilogue of one tile while the next is multiplied (sixteen, so
+// that the last tile's, which nothing hides, is short).  Every wait is bounded
+// (E4B_ERR_TIMEOUT in the status word).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,7 +36,7 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int BM = 128;                  // rows of D per CTA
 constexpr int BK = 64;                   // K per stage: one 128-byte swizzle row of bf16
-constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, EPI_WARPS = 8;
+constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, EPI_WARPS = 16;
 constexpr int THREADS = 32 * (WARP_EPI0 + EPI_WARPS);
 constexpr uint64_t kDrainNs = 50000000ull;
 constexpr int kGroupM = 16;              // row tiles that share a sweep over the columns (L2 reuse of both operands)
@@ -56,12 +57,14 @@ struct Cfg {
 
 struct Params {
   int32_t M, N, K;          // D is M x N; gate_up: N = I features (2I rows of B)
+  int32_t width;            // columns of D per tile, a multiple of 32, at most BN
   int32_t m_tiles, n_tiles;
   int32_t act;
   float alpha, limit, beta;
   const float* bias;        // gate_up: [2I]; linear: [N]; or null
   int32_t bias_words;       // bias is 16-byte aligned
   const uint16_t* add;      // linear: [M, N] bf16 or null
+  int32_t wide;             // rows of out are whole 32-byte words
   uint16_t* out;            // bf16: h [M, I], D [M, N] or dG [M, 2I]
   float* g_out;             // gate_up: G [M, 2I] fp32 or null
   const float* g_in;        // dact: G [M, 2I]
@@ -99,8 +102,33 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void store8(uint16_t* o, const float* f) {
-  *reinterpret_cast<uint4*>(o) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+// 32-byte accesses: in the row-per-lane layout of a tensor-memory load every lane touches its own row, and a whole
+// sector per lane halves the requests.
+__device__ __forceinline__ void store32(void* o, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+
+// Sixteen adjacent bf16 columns of one row, or the first eight of them (the last of a ragged row).
+__device__ __forceinline__ void store16(uint16_t* o, const uint4 (&v)[2], bool both, bool wide) {
+  if (both && wide) {
+    store32(o, v[0], v[1]);
+  } else {
+    *reinterpret_cast<uint4*>(o) = v[0];
+    if (both) *reinterpret_cast<uint4*>(o + 8) = v[1];
+  }
 }
 
 // d(act)/d(gate) and d(act)/d(up); the clamps pass the gradient inside their range, ends included.
@@ -155,18 +183,28 @@ __device__ __forceinline__ void add_bias8(const Params& p, int at, float (&f)[8]
   }
 }
 
+// Eight fp32 values of G (its rows are whole 32-byte words: 2I is a multiple of 16).
 __device__ __forceinline__ void store8f(float* o, const float (&f)[8]) {
-  reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  uint4 a, b;
+  a.x = __float_as_uint(f[0]); a.y = __float_as_uint(f[1]); a.z = __float_as_uint(f[2]); a.w = __float_as_uint(f[3]);
+  b.x = __float_as_uint(f[4]); b.y = __float_as_uint(f[5]); b.z = __float_as_uint(f[6]); b.w = __float_as_uint(f[7]);
+  store32(o, a, b);
 }
 
-// The epilogues, eight adjacent columns of one row at a time (fp32 sums in, `col` a multiple of 8, below N).
-__device__ __forceinline__ void finish_gate_up(const Params& p, int row, bool row_in, int col, float (&g)[8],
-                                               float (&u)[8]) {
+__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+  uint4 a, b;
+  load32(p, a, b);
+  f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+  f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+}
+
+// The epilogues, eight adjacent columns of one row at a time (fp32 sums in, `col` a multiple of 8, below N), packed
+// to bf16.  Rows past M hold zeros and are not read or written.
+__device__ __forceinline__ uint4 finish_gate_up(const Params& p, int row, bool row_in, int col, float (&g)[8],
+                                                float (&u)[8]) {
   add_bias8(p, col, g);
   add_bias8(p, p.N + col, u);
-  if (!row_in) return;
-  if (p.g_out) {
+  if (p.g_out && row_in) {
     float* o = p.g_out + static_cast<int64_t>(row) * 2 * p.N + col;
     store8f(o, g);
     store8f(o + p.N, u);
@@ -174,15 +212,13 @@ __device__ __forceinline__ void finish_gate_up(const Params& p, int row, bool ro
   const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
 #pragma unroll
   for (int i = 0; i < 8; ++i) g[i] = expert_act(ep, g[i], u[i]);
-  store8(p.out + static_cast<int64_t>(row) * p.N + col, g);
+  return pack8(g);
 }
 
-__device__ __forceinline__ void finish_linear(const Params& p, int row, bool row_in, int col, float (&f)[8]) {
+__device__ __forceinline__ uint4 finish_linear(const Params& p, int row, bool row_in, int col, float (&f)[8]) {
   add_bias8(p, col, f);
-  if (!row_in) return;
-  const int64_t at = static_cast<int64_t>(row) * p.N + col;
-  if (p.add) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p.add + at);
+  if (p.add && row_in) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p.add + static_cast<int64_t>(row) * p.N + col);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -190,34 +226,29 @@ __device__ __forceinline__ void finish_linear(const Params& p, int row, bool row
       f[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-  store8(p.out + at, f);
+  return pack8(f);
 }
 
 // All lanes of the warp call it with rows row0 + lane (row0 a multiple of 32).
 __device__ __forceinline__ void finish_dact(const Params& p, int row, bool row_in, int col, int lane,
-                                            const float (&dh)[8]) {
+                                            const float (&dh)[8], uint4& og, uint4& ou) {
   float dg[8], du[8];
 #pragma unroll
-  for (int j = 0; j < 8; j += 4) {
-    float4 fg = make_float4(0.f, 0.f, 0.f, 0.f), fu = fg;
-    if (row_in) {
-      const float* gp = p.g_in + static_cast<int64_t>(row) * 2 * p.N + col + j;
-      fg = *reinterpret_cast<const float4*>(gp);
-      fu = *reinterpret_cast<const float4*>(gp + p.N);
-    }
-    const float gv[4] = {fg.x, fg.y, fg.z, fg.w}, uv[4] = {fu.x, fu.y, fu.z, fu.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      act_grads(p, gv[i], uv[i], dg[j + i], du[j + i]);
-      dg[j + i] = row_in ? dg[j + i] * dh[j + i] : 0.0f;
-      du[j + i] = row_in ? du[j + i] * dh[j + i] : 0.0f;
-    }
-  }
+  for (int i = 0; i < 8; ++i) dg[i] = du[i] = 0.0f;
   if (row_in) {
-    uint16_t* o = p.out + static_cast<int64_t>(row) * 2 * p.N + col;
-    store8(o, dg);
-    store8(o + p.N, du);
+    float g[8], u[8];
+    const float* gp = p.g_in + static_cast<int64_t>(row) * 2 * p.N + col;
+    load8f(gp, g);
+    load8f(gp + p.N, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      act_grads(p, g[i], u[i], dg[i], du[i]);
+      dg[i] *= dh[i];
+      du[i] *= dh[i];
+    }
   }
+  og = pack8(dg);
+  ou = pack8(du);
   if (p.colsum) {                         // from the fp32 values, before their rounding to bf16
     const int row0 = row - lane;
     int c;
@@ -288,7 +319,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const WaitCtx wctx{s_abort, p.status, p.wait_limit_ns};
   const int total = p.m_tiles * p.n_tiles;
   const int ksteps = (p.K + BK - 1) / BK;
-  constexpr int NT = EPI == kEpiGateUp ? BN / 2 : BN;   // output columns (features) per tile
+  const int NT = EPI == kEpiGateUp ? p.width / 2 : p.width;     // output columns (features) per tile
+  const int b_rows = p.width / CG;                              // this CTA's rows of B per stage
+  const int b_boxes = (b_rows + 63) / 64;                       // B row-contiguous: whole boxes of 64
+  const uint32_t stage_tx = C::A_BYTES + (B_MN ? b_boxes * 8192 : b_rows * BK * 2);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == WARP_TMA) {
@@ -302,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int ks = 0; ks < ksteps; ++ks) {
         if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wctx, 1101)) { ok = false; break; }
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * stage_tx);
           const uint32_t bar = CG == 2 ? cluster_addr(&full[stage], 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
             if constexpr (CG == 2) tma_load_2d_pair(dst, map, bar, x, y);
@@ -317,15 +351,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else {
             load(a, &tm_a, k0, m0);
           }
-          const int nb = n0 + static_cast<int>(rank) * C::B_ROWS;
+          const int nb = n0 + static_cast<int>(rank) * b_rows;
           if constexpr (EPI == kEpiGateUp && CG == 2) {  // gate rows in one CTA, the matching up rows in the other
             load(b, &tm_b, k0, rank == 0 ? n0 : p.N + n0);
           } else if constexpr (EPI == kEpiGateUp) {      // gate rows, then the matching up rows
             load(b, &tm_b, k0, n0);
             load(b + NT * BK * 2, &tm_b, k0, p.N + n0);
           } else if constexpr (B_MN) {
-#pragma unroll
-            for (int i = 0; i < C::B_ROWS / 64; ++i) load(b + i * 8192, &tm_b, nb + 64 * i, k0);
+            for (int i = 0; i < b_boxes; ++i) load(b + i * 8192, &tm_b, nb + 64 * i, k0);
           } else {
             load(b, &tm_b, k0, nb);
           }
@@ -342,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == WARP_MMA) {
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(CG * BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      const uint32_t idesc = idesc_bf16_f32(CG * BM, p.width) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
       // descriptors differ only in their start address (16-byte units): 16 of K are 32 bytes along a row, or two
       // 8-row atoms where K is the row
       const uint32_t base = smem_u32(smem);
@@ -388,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= WARP_EPI0) {
     const int q = warp & 3;                        // TMEM lanes 32q..32q+31: D row = lane
-    const int half = (warp - WARP_EPI0) >> 2;      // this warp's half of the columns
+    const int part = (warp - WARP_EPI0) >> 2;      // the warps of a row quarter take chunks of 16 columns in turn
     int it = 0;
     for (int tile = first; tile < total; tile += step, ++it) {
       int mt, nt;
@@ -402,27 +435,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row = row0 + lane;
       const bool row_in = row < p.M;
 #pragma unroll 1
-      for (int c0 = half * (NT / 2); c0 < (half + 1) * (NT / 2); c0 += 16) {
+      for (int c0 = 16 * part; c0 < NT; c0 += 16 * (EPI_WARPS / 4)) {
         const int col = nt * NT + c0;
         if (col >= p.N) break;
         uint32_t r[16], u[16];
         tmem_ld_32x32b_x16(taddr + c0, r);
         if constexpr (EPI == kEpiGateUp) tmem_ld_32x32b_x16(taddr + NT + c0, u);
         tmem_ld_wait();
+        const bool both = col + 8 < p.N;               // (a tile's width is a multiple of 16)
+        uint4 v[2], w[2];
 #pragma unroll
-        for (int j = 0; j < 16; j += 8) {
-          if (col + j >= p.N) break;
+        for (int j = 0; j < 2; ++j) {
+          if (j == 1 && !both) break;
           float f[8];
-          take8(r, j, f);
+          take8(r, 8 * j, f);
           if constexpr (EPI == kEpiGateUp) {
             float fu[8];
-            take8(u, j, fu);
-            finish_gate_up(p, row, row_in, col + j, f, fu);
+            take8(u, 8 * j, fu);
+            v[j] = finish_gate_up(p, row, row_in, col + 8 * j, f, fu);
           } else if constexpr (EPI == kEpiLinear) {
-            finish_linear(p, row, row_in, col + j, f);
+            v[j] = finish_linear(p, row, row_in, col + 8 * j, f);
           } else {
-            finish_dact(p, row, row_in, col + j, lane, f);
+            finish_dact(p, row, row_in, col + 8 * j, lane, f, v[j], w[j]);
           }
+        }
+        if (row_in) {
+          uint16_t* o = p.out + static_cast<int64_t>(row) * (EPI == kEpiDact ? 2 * p.N : p.N) + col;
+          store16(o, v, both, p.wide);
+          if constexpr (EPI == kEpiDact) store16(o + p.N, w, both, p.wide);
         }
       }
       tc_fence_before_sync();
@@ -466,7 +506,8 @@ struct SplitCfg {
   static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 1) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-  static_assert(OFF_SUMS + EPI_WARPS * 2 * BN * 4 <= STAGES * STAGE_BYTES, "both reuse the stages");
+  static constexpr int EPI = 8, THREADS = 32 * (WARP_EPI0 + EPI);
+  static_assert(OFF_SUMS + EPI * 2 * BN * 4 <= STAGES * STAGE_BYTES, "both reuse the stages");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -491,7 +532,7 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 __device__ __forceinline__ uint2 pack4(const float4& v) { return make_uint2(pack2(v.x, v.y), pack2(v.z, v.w)); }
 
 template <bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     dense_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                        const Params p, int S) {
   using C = SplitCfg;
@@ -657,7 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (EPI != kEpiDact && p.bias && col_in) bias = bias4(p, EPI == kEpiGateUp && lane >= 16 ? p.N + col : col);
     float4 sg = make_float4(0.f, 0.f, 0.f, 0.f), su = sg;      // dact: column sums over this warp's rows
 #pragma unroll 2
-    for (int r = rank + S * ew; r < rows; r += S * EPI_WARPS) {
+    for (int r = rank + S * ew; r < rows; r += S * C::EPI) {
       const int64_t row = m0 + r;
       float4 f = bias;
 #pragma unroll 4
@@ -712,11 +753,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         float4* sums = reinterpret_cast<float4*>(smem + C::OFF_SUMS);
         sums[ew * 64 + lane] = sg;
         sums[ew * 64 + 32 + lane] = su;
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::EPI) : "memory");
         const int i = threadIdx.x - 32 * WARP_EPI0;
         if (i < 64) {
           float4 t = sums[i];
-          for (int w = 1; w < EPI_WARPS; ++w) add4(t, sums[w * 64 + i]);
+          for (int w = 1; w < C::EPI; ++w) add4(t, sums[w * 64 + i]);
           const int c = n0 + 4 * (i & 31);
           if (c < p.N)
             *reinterpret_cast<float4*>(p.colsum + (static_cast<int64_t>(mt) * S + rank) * 2 * p.N + (i >> 5) * p.N + c) = t;
@@ -746,11 +787,12 @@ bool encode_operands(const DenseGemmLaunch& g, int b_box, CUtensorMap* ta, CUten
   return enc(ta, g.a, g.M, g.K, A_MN, BM) && enc(tb, g.b, b_rows, g.K, B_MN, b_box);
 }
 
-Params make_params(const DenseGemmLaunch& g, int tile_rows, int tile_cols) {
+Params make_params(const DenseGemmLaunch& g, int tile_rows, int width, int tile_cols) {
   Params p;
   p.M = g.M;
   p.N = g.N;
   p.K = g.K;
+  p.width = width;
   p.m_tiles = (g.M + tile_rows - 1) / tile_rows;
   p.n_tiles = (g.N + tile_cols - 1) / tile_cols;
   p.act = g.act;
@@ -761,6 +803,7 @@ Params make_params(const DenseGemmLaunch& g, int tile_rows, int tile_cols) {
   p.bias_words = aligned(g.bias, 16) ? 1 : 0;
   p.add = g.add;
   p.out = g.out;
+  p.wide = g.N % 16 == 0 && aligned(g.out, 32) ? 1 : 0;
   p.g_out = g.g_out;
   p.g_in = g.g_in;
   p.colsum = g.colsum;
@@ -778,16 +821,16 @@ cudaError_t allow_smem(K kern, int bytes, std::once_flag& once, cudaError_t& err
 }
 
 template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
-e4b_status launch_typed(const DenseGemmLaunch& g, cudaStream_t s) {
+e4b_status launch_typed(const DenseGemmLaunch& g, int width, cudaStream_t s) {
   using C = Cfg<BN, CG>;
   auto kern = dense_gemm_kernel<BN, CG, A_MN, B_MN, EPI>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   if (allow_smem(kern, C::SMEM_BYTES, once, attr_err) != cudaSuccess) return E4B_ERR_CUDA;
-  constexpr int NT = EPI == kEpiGateUp ? BN / 2 : BN;
+  const int NT = EPI == kEpiGateUp ? width / 2 : width;
   CUtensorMap ta, tb;
-  if (!encode_operands<A_MN, B_MN, EPI>(g, EPI == kEpiGateUp ? NT : C::B_ROWS, &ta, &tb)) return E4B_ERR_CUDA;
-  const Params p = make_params(g, CG * BM, NT);
+  if (!encode_operands<A_MN, B_MN, EPI>(g, EPI == kEpiGateUp ? NT : width / CG, &ta, &tb)) return E4B_ERR_CUDA;
+  const Params p = make_params(g, CG * BM, width, NT);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   const int64_t slots = device_sm_count() / CG;
   const dim3 grid(static_cast<unsigned>(CG * (tiles < slots ? tiles : slots)));
@@ -811,7 +854,7 @@ int split_slots(int S) {
   if (n > 0) return n - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(S));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -829,19 +872,20 @@ e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
   constexpr int NT = EPI == kEpiGateUp ? SplitCfg::BN / 2 : SplitCfg::BN;
   CUtensorMap ta, tb;
   if (!encode_operands<A_MN, B_MN, EPI>(g, NT, &ta, &tb)) return E4B_ERR_CUDA;
-  const Params p = make_params(g, BM, NT);
+  const Params p = make_params(g, BM, SplitCfg::BN, NT);
   if (g.colsum_rows) *g.colsum_rows = p.m_tiles * S;
   const dim3 grid(static_cast<unsigned>(p.m_tiles * p.n_tiles * S));
-  return launch_pdl_cluster(static_cast<unsigned>(S), dense_split_kernel<A_MN, B_MN, EPI>, grid, dim3(THREADS),
+  return launch_pdl_cluster(static_cast<unsigned>(S), dense_split_kernel<A_MN, B_MN, EPI>, grid, dim3(SplitCfg::THREADS),
                             SplitCfg::SMEM_BYTES, s, ta, tb, p, S) == cudaSuccess
              ? E4B_OK
              : E4B_ERR_CUDA;
 }
 
 // Which kernel: estimated time in units of one 64-K step of a 256 x 256 pair
-// tile (0.28 us on a B200).  A step of a 128 x 128 tile of one CTA costs 0.8 of
-// that (issue-bound, whatever its width), a 128-K step of the split kernel 1.7
-// (it waits for its loads) and its exchange about 6.
+// tile (0.28 us on a B200).  A narrower pair tile costs nearly its share, so a
+// width that fills the last wave of pairs may win over 256.  A step of a
+// 128 x 128 tile of one CTA costs 0.8 (issue-bound, whatever its width), a 128-K
+// step of the split kernel 1.7 (it waits for its loads) and its exchange about 6.
 template <bool A_MN, bool B_MN, int EPI>
 e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
   const int64_t sms = device_sm_count();
@@ -851,7 +895,15 @@ e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
   };
   auto waves = [](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
   const int64_t k64 = (g.K + BK - 1) / BK, k128 = (g.K + 127) / 128, t128 = tiles(128, 128);
-  const double pair = waves(tiles(256, 256), sms / 2) * k64 + 4.0;
+  int width = 256;
+  double pair = waves(tiles(256, 256), sms / 2) * k64 + 4.0;
+  for (int w = 224; w >= 160; w -= 32) {
+    const double t = waves(tiles(256, w), sms / 2) * k64 * (0.1 + 0.9 * w / 256.0) + 4.0;
+    if (t < 0.97 * pair) {
+      pair = t;
+      width = w;
+    }
+  }
   const double single = waves(t128, sms) * k64 * 0.8;
   double best = pair < single ? pair : single;
   int S = 1;
@@ -864,8 +916,8 @@ e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
   }
   if (S > 1) return launch_split<A_MN, B_MN, EPI>(g, S, s);
   if (g.colsum_rows) *g.colsum_rows = (g.M + 31) / 32;
-  if (pair < single) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, s);
-  return launch_typed<128, 1, A_MN, B_MN, EPI>(g, s);
+  if (pair < single) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, width, s);
+  return launch_typed<128, 1, A_MN, B_MN, EPI>(g, 128, s);
 }
 
 }  // namespace

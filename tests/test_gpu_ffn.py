@@ -93,7 +93,9 @@ SHAPES = [(1, 8, 8), (1, 2048, 768), (2, 64, 128), (7, 72, 200), (8, 264, 40), (
           (17, 8, 8), (17, 64, 128), (31, 72, 200), (32, 200, 72), (33, 264, 776), (127, 512, 64), (128, 64, 512),
           (129, 128, 136), (300, 520, 296), (1000, 136, 2440), (700, 1400, 2808), (2050, 264, 1160),
           # each product of the pair in turn on CTA pairs, with ragged rows and columns
-          (2050, 72, 2312), (2050, 2312, 72), (40, 2568, 2008)]
+          (2050, 72, 2312), (2050, 2312, 72), (40, 2568, 2008),
+          # narrower pair tiles, chosen where they fill the last wave
+          (3300, 1800, 640), (3300, 640, 1800), (640, 3400, 1800)]
 
 
 @pytest.mark.parametrize("T,H,I", SHAPES)
