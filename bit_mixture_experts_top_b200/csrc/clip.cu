@@ -11,9 +11,10 @@
 // needs no clearing.  Squares are formed and summed in fp64, so values whose
 // square leaves the fp32 range still count (a gradient of 1e25, or of 1e-30).
 //
-// Both passes are bound by HBM.  Work is dealt in chunks of 16 KB: four 16-byte
-// loads per thread, eight blocks per SM.  The second pass walks the chunks from
-// the last to the first, so that what the first pass read last is still in L2.
+// Both passes are bound by HBM.  Work is dealt in chunks of 16 KB (32 KB in long
+// lists): four (eight) 16-byte loads per thread, eight blocks per SM.  The
+// second pass walks the chunks from the last to the first, so that what the
+// first pass read last is still in L2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,9 +29,10 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kVecPerThread = 4;
-constexpr int kChunkVecs = kThreads * kVecPerThread;   // 16-byte words per chunk
+constexpr int kSmall = 64, kMedium = 256, kMaxTable = 960;   // 2, 8 and 30 KB of kernel arguments
 constexpr int kBlocksPerSm = 8;
+__host__ __device__ constexpr int words_per_thread(bool is_long) { return is_long ? 8 : 4; }   // 16-byte words per chunk
+constexpr size_t kLongBytes = size_t(160) << 20;   // a launch's tensors from which on chunks are long and strided
 
 // One tensor of the table.  Its 16-byte words start at the boundary at or
 // below the first element; `skip` elements of the first word are not its own.
@@ -46,21 +48,66 @@ struct ClipEntry {
 
 template <int N>
 struct ClipTable {
-  int32_t tensors, chunks;
+  int32_t tensors, chunks, strided;
   ClipEntry e[N];
 };
 
 template <int TYPE>
 __host__ __device__ constexpr int size_of() { return TYPE == E4B_F32 ? 4 : 2; }
 
+// Which tensor a chunk belongs to, by bisection in shared memory (the table itself lies in the argument bank, whose
+// cache misses cost more than the search).
 template <int N>
-__device__ __forceinline__ int tensor_of(const ClipTable<N>& t, int chunk) {
-  int lo = 0, hi = t.tensors;             // last tensor with chunk0 <= chunk
+struct ChunkIndex {
+  int32_t first[N];
+
+  __device__ __forceinline__ void fill(const ClipTable<N>& t) {   // (a warp reads one entry at a time: lanes that
+    for (int i = threadIdx.x >> 5; i < t.tensors; i += kThreads / 32)   // differ would be served one by one)
+      if ((threadIdx.x & 31) == 0) first[i] = t.e[i].chunk0;
+    __syncthreads();
+  }
+};
+
+// The last tensor whose first chunk, first_of(i), is at or before this one.
+template <typename First>
+__device__ __forceinline__ int tensor_of(int tensors, int chunk, const First& first_of) {
+  int lo = 0, hi = tensors;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (t.e[mid].chunk0 <= chunk) lo = mid; else hi = mid;
+    if (first_of(mid) <= chunk) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// Walks a block's chunks, calling body(entry, chunk).  LONG lists: strided over
+// the whole list, so that the blocks move through memory together, the tensor
+// found anew for each chunk.  Short lists, mostly of small tensors: one
+// contiguous run, whose next chunk lies in the same tensor or the one beside it.
+// REVERSED: the same chunks from the last to the first.
+template <int N, bool LONG, bool REVERSED, typename Index, typename Body>
+__device__ __forceinline__ void walk_chunks(const ClipTable<N>& t, const Index& index, const Body& body) {
+  const int b = blockIdx.x, n = gridDim.x;
+  if constexpr (LONG) {
+    const int count = b < t.chunks ? (t.chunks - 1 - b) / n + 1 : 0;
+    for (int i = 0; i < count; ++i) {
+      const int c = b + (REVERSED ? count - 1 - i : i) * n;
+      body(t.e[tensor_of(t.tensors, c, [&](int j) { return index.first[j]; })], c);
+    }
+  } else {
+    const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * b / n);
+    const int c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (b + 1) / n);
+    if (c0 == c1) return;
+    int ti = tensor_of(t.tensors, REVERSED ? c1 - 1 : c0, [&](int j) { return t.e[j].chunk0; });
+    for (int i = 0; i < c1 - c0; ++i) {
+      const int c = REVERSED ? c1 - 1 - i : c0 + i;
+      if constexpr (REVERSED) {
+        while (t.e[ti].chunk0 > c) --ti;
+      } else {
+        while (ti + 1 < t.tensors && t.e[ti + 1].chunk0 <= c) ++ti;
+      }
+      body(t.e[ti], c);
+    }
+  }
 }
 
 // The elements of one 16-byte word as fp32.
@@ -122,22 +169,22 @@ __device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
 // Calls word(i) for this thread's words of the chunk that lie wholly inside the
 // tensor and one(k) for the single elements of its first and last word.  A
 // chunk in the tensor's middle is only whole words and takes no tests.
-template <int TYPE, typename Word, typename One>
+template <int TYPE, int V, typename Word, typename One>
 __device__ __forceinline__ void for_chunk(const ClipEntry& e, int64_t w0, const Word& word, const One& one) {
   constexpr int PER = 16 / size_of<TYPE>();
   const int64_t last = e.n + e.skip;                      // elements counted from the first word's start
   const int64_t c0 = w0 - threadIdx.x;
-  if (c0 * PER >= e.skip && (c0 + kChunkVecs) * PER <= last) {
-    uint4 v[kVecPerThread];
+  if (c0 * PER >= e.skip && (c0 + V * kThreads) * PER <= last) {
+    uint4 v[V];
     const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>()) + w0;
 #pragma unroll
-    for (int i = 0; i < kVecPerThread; ++i) v[i] = in[i * kThreads];
+    for (int i = 0; i < V; ++i) v[i] = in[i * kThreads];
 #pragma unroll
-    for (int i = 0; i < kVecPerThread; ++i) word(w0 + i * kThreads, v[i]);
+    for (int i = 0; i < V; ++i) word(w0 + i * kThreads, v[i]);
     return;
   }
   const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>());
-  for (int i = 0; i < kVecPerThread; ++i) {
+  for (int i = 0; i < V; ++i) {
     const int64_t w = w0 + i * kThreads, at = w * PER;
     if (at >= last) break;
     if (at >= e.skip && at + PER <= last) {
@@ -149,10 +196,10 @@ __device__ __forceinline__ void for_chunk(const ClipEntry& e, int64_t w0, const 
   }
 }
 
-template <int TYPE>
+template <int TYPE, int V>
 __device__ __forceinline__ double chunk_squares(const ClipEntry& e, int64_t w0) {
   double sum = 0.0;
-  for_chunk<TYPE>(
+  for_chunk<TYPE, V>(
       e, w0,
       [&](int64_t, const uint4& v) {
         float f[16 / size_of<TYPE>()];
@@ -168,11 +215,11 @@ __device__ __forceinline__ double chunk_squares(const ClipEntry& e, int64_t w0) 
   return sum;
 }
 
-template <int TYPE>
+template <int TYPE, int V>
 __device__ __forceinline__ void chunk_scale(const ClipEntry& e, int64_t w0, float c) {
   constexpr int PER = 16 / size_of<TYPE>();
   uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(e.out) - e.skip * size_of<TYPE>());
-  for_chunk<TYPE>(
+  for_chunk<TYPE, V>(
       e, w0,
       [&](int64_t w, const uint4& v) {
         if (e.words) {
@@ -198,59 +245,55 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return t;
 }
 
-template <int N>
+template <int N, bool LONG>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ ClipTable<N> t,
                                                              double* __restrict__ partial) {
   __shared__ double red[kThreads / 32];
+  __shared__ ChunkIndex<LONG ? N : 1> index;
+  if constexpr (LONG) index.fill(t);
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int V = words_per_thread(LONG);
   double sum = 0.0;
-  const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * blockIdx.x / gridDim.x);
-  const int c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
-  int ti = tensor_of(t, c0);
-  for (int c = c0; c < c1; ++c) {
-    while (ti + 1 < t.tensors && t.e[ti + 1].chunk0 <= c) ++ti;
-    const ClipEntry& e = t.e[ti];
-    const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * kChunkVecs + threadIdx.x;
-    if (e.type == E4B_F32) sum += chunk_squares<E4B_F32>(e, w0);
-    else if (e.type == E4B_BF16) sum += chunk_squares<E4B_BF16>(e, w0);
-    else sum += chunk_squares<E4B_F16>(e, w0);
-  }
+  walk_chunks<N, LONG, false>(t, index, [&](const ClipEntry& e, int c) {
+    const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * (V * kThreads) + threadIdx.x;
+    if (e.type == E4B_F32) sum += chunk_squares<E4B_F32, V>(e, w0);
+    else if (e.type == E4B_BF16) sum += chunk_squares<E4B_BF16, V>(e, w0);
+    else sum += chunk_squares<E4B_F16, V>(e, w0);
+  });
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
 // max_norm is +infinity where only the norm is wanted.
-template <int N>
+template <int N, bool LONG>
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipTable<N> t,
                                                               const double* __restrict__ partial, int partials,
                                                               double max_norm, float* __restrict__ total_norm) {
   __shared__ double red[kThreads / 32];
+  __shared__ ChunkIndex<LONG ? N : 1> index;
+  if constexpr (LONG) index.fill(t);
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int V = words_per_thread(LONG);
   double sum = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
   const double norm = sqrt(block_sum(sum, red));
   if (total_norm && blockIdx.x == 0 && threadIdx.x == 0) *total_norm = static_cast<float>(norm);
   const double ratio = max_norm / (norm + 1e-6);
   const float coef = isinf(max_norm) || ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);   // a NaN norm gives NaN
-  const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * blockIdx.x / gridDim.x);
-  const int c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
-  if (c0 == c1) return;
-  int ti = tensor_of(t, c1 - 1);
-  for (int c = c1 - 1; c >= c0; --c) {
-    while (t.e[ti].chunk0 > c) --ti;
-    const ClipEntry& e = t.e[ti];
-    if (e.in == e.out && coef == 1.0f) continue;          // in place and unclipped: already there
-    const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * kChunkVecs + threadIdx.x;
-    if (e.type == E4B_F32) chunk_scale<E4B_F32>(e, w0, coef);
-    else if (e.type == E4B_BF16) chunk_scale<E4B_BF16>(e, w0, coef);
-    else chunk_scale<E4B_F16>(e, w0, coef);
-  }
+  walk_chunks<N, LONG, true>(t, index, [&](const ClipEntry& e, int c) {
+    if (e.in == e.out && coef == 1.0f) return;            // in place and unclipped: already there
+    const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * (V * kThreads) + threadIdx.x;
+    if (e.type == E4B_F32) chunk_scale<E4B_F32, V>(e, w0, coef);
+    else if (e.type == E4B_BF16) chunk_scale<E4B_BF16, V>(e, w0, coef);
+    else chunk_scale<E4B_F16, V>(e, w0, coef);
+  });
 }
 
 template <int N>
-void fill_table(ClipTable<N>& t, const e4b_grad* g, int count) {
+void fill_table(ClipTable<N>& t, const e4b_grad* g, int count, bool is_long) {
+  const int64_t chunk_bytes = 16 * kThreads * words_per_thread(is_long);
   t.tensors = count;
   int64_t chunk = 0;
   for (int i = 0; i < count; ++i) {
@@ -264,7 +307,7 @@ void fill_table(ClipTable<N>& t, const e4b_grad* g, int count) {
     e.skip = static_cast<int8_t>((a % 16) / size);
     e.words = reinterpret_cast<uintptr_t>(g[i].out) % 16 == a % 16;
     e.chunk0 = static_cast<int32_t>(chunk);
-    if (e.n > 0) chunk += ((e.n + e.skip) * size + kChunkVecs * 16 - 1) / (kChunkVecs * 16);
+    if (e.n > 0) chunk += ((e.n + e.skip) * size + chunk_bytes - 1) / chunk_bytes;
   }
   t.chunks = static_cast<int32_t>(chunk);
 }
@@ -274,24 +317,39 @@ int blocks_for(int chunks) {
   return chunks < cap ? (chunks > 0 ? chunks : 1) : cap;
 }
 
-template <int N>
-cudaError_t run_norm(const e4b_grad* g, int count, double* partial, int* blocks, cudaStream_t s) {
-  ClipTable<N> t;
-  fill_table(t, g, count);
-  *blocks = blocks_for(t.chunks);
-  return launch_pdl(grad_norm_kernel<N>, dim3(*blocks), dim3(kThreads), 0, s, t, partial);
-}
+// Both kernels for `count` tensors; partial and the count of what is in it move on with the norm pass.
+struct ClipRun {
+  const e4b_grad* g;
+  int count;
+  bool is_long;
+  cudaStream_t s;
 
-template <int N>
-cudaError_t run_scale(const e4b_grad* g, int count, const double* partial, int partials, double max_norm,
-                      float* total_norm, cudaStream_t s) {
-  ClipTable<N> t;
-  fill_table(t, g, count);
-  return launch_pdl(grad_scale_kernel<N>, dim3(blocks_for(t.chunks)), dim3(kThreads), 0, s, t, partial, partials,
-                    max_norm, total_norm);
-}
-
-constexpr int kSmall = 64, kMedium = 256, kMaxTable = 960;   // 2, 8 and 30 KB of kernel arguments
+  template <int N, bool LONG>
+  cudaError_t norm(double* partial, int* blocks) const {
+    ClipTable<N> t;
+    fill_table(t, g, count, LONG);
+    *blocks = blocks_for(t.chunks);
+    return launch_pdl(grad_norm_kernel<N, LONG>, dim3(*blocks), dim3(kThreads), 0, s, t, partial);
+  }
+  template <int N, bool LONG>
+  cudaError_t scale(const double* partial, int partials, double max_norm, float* total_norm) const {
+    ClipTable<N> t;
+    fill_table(t, g, count, LONG);
+    return launch_pdl(grad_scale_kernel<N, LONG>, dim3(blocks_for(t.chunks)), dim3(kThreads), 0, s, t, partial,
+                      partials, max_norm, total_norm);
+  }
+  cudaError_t norm(double* partial, int* blocks) const {
+    if (count <= kSmall) return is_long ? norm<kSmall, true>(partial, blocks) : norm<kSmall, false>(partial, blocks);
+    if (count <= kMedium) return is_long ? norm<kMedium, true>(partial, blocks) : norm<kMedium, false>(partial, blocks);
+    return is_long ? norm<kMaxTable, true>(partial, blocks) : norm<kMaxTable, false>(partial, blocks);
+  }
+  cudaError_t scale(const double* p, int n, double max_norm, float* out) const {
+    if (count <= kSmall) return is_long ? scale<kSmall, true>(p, n, max_norm, out) : scale<kSmall, false>(p, n, max_norm, out);
+    if (count <= kMedium)
+      return is_long ? scale<kMedium, true>(p, n, max_norm, out) : scale<kMedium, false>(p, n, max_norm, out);
+    return is_long ? scale<kMaxTable, true>(p, n, max_norm, out) : scale<kMaxTable, false>(p, n, max_norm, out);
+  }
+};
 
 }  // namespace
 
@@ -302,31 +360,28 @@ size_t grad_norm_partials(int32_t tensors) {
 
 cudaError_t launch_clip_grads(const e4b_grad* g, int32_t tensors, double max_norm, float* total_norm, double* partial,
                               cudaStream_t s) {
-  int partials = 0, i = 0;
-  do {
-    const int n = tensors - i < kMaxTable ? tensors - i : kMaxTable;
+  bool in_place = true;
+  auto run_at = [&](int32_t i) {
+    ClipRun r{g + i, tensors - i < kMaxTable ? tensors - i : kMaxTable, false, s};
+    size_t bytes = 0;
+    for (int k = 0; k < r.count; ++k) bytes += static_cast<size_t>(r.g[k].n) * (r.g[k].dtype == E4B_F32 ? 4 : 2);
+    r.is_long = bytes >= kLongBytes;
+    return r;
+  };
+  int partials = 0;
+  for (int32_t i = 0; i == 0 || i < tensors; i += kMaxTable) {
     int blocks = 0;
-    const cudaError_t e = n <= kSmall    ? run_norm<kSmall>(g + i, n, partial + partials, &blocks, s)
-                          : n <= kMedium ? run_norm<kMedium>(g + i, n, partial + partials, &blocks, s)
-                                         : run_norm<kMaxTable>(g + i, n, partial + partials, &blocks, s);
+    const cudaError_t e = run_at(i).norm(partial + partials, &blocks);
     if (e != cudaSuccess) return e;
     partials += blocks;
-    i += n;
-  } while (i < tensors);
-  bool in_place = true;
+  }
   for (int32_t k = 0; k < tensors; ++k) in_place = in_place && (g[k].n == 0 || g[k].grad == g[k].out);
   // only the norm is wanted and nothing moves: one block writes it
-  if (std::isinf(max_norm) && in_place) return run_scale<kSmall>(g, 0, partial, partials, max_norm, total_norm, s);
-  i = 0;
-  do {
-    const int n = tensors - i < kMaxTable ? tensors - i : kMaxTable;
-    float* out = i == 0 ? total_norm : nullptr;
-    const cudaError_t e = n <= kSmall    ? run_scale<kSmall>(g + i, n, partial, partials, max_norm, out, s)
-                          : n <= kMedium ? run_scale<kMedium>(g + i, n, partial, partials, max_norm, out, s)
-                                         : run_scale<kMaxTable>(g + i, n, partial, partials, max_norm, out, s);
+  if (std::isinf(max_norm) && in_place) return ClipRun{g, 0, false, s}.scale(partial, partials, max_norm, total_norm);
+  for (int32_t i = 0; i == 0 || i < tensors; i += kMaxTable) {
+    const cudaError_t e = run_at(i).scale(partial, partials, max_norm, i == 0 ? total_norm : nullptr);
     if (e != cudaSuccess) return e;
-    i += n;
-  } while (i < tensors);
+  }
   return cudaSuccess;
 }
 

@@ -75,6 +75,27 @@ def test_packed_without_alignment(types):
             assert bool((dst[t].cpu()[~used[t]] == 9).all())
 
 
+def test_long_lists():
+    # over 160 MB the blocks stride over the list; whole and ragged tensors, all types, unaligned ones among them
+    sizes = [25_000_003, 1, 17_000_001, 33, 0, 1 << 20, 12_345_679]
+    flat = {t: (torch.randn(30_000_000, generator=torch.Generator(device="cuda").manual_seed(5), device=device())).to(t) for t in TYPES}
+    grads, at = [], {t: i for i, t in enumerate(TYPES)}
+    for i, n in enumerate(sizes):
+        t = TYPES[0] if i in (0, 2) else TYPES[i % 3]
+        start = 0 if n > 30_000_000 - at[t] - n else at[t]
+        grads.append((torch.randn(n + 1, generator=torch.Generator(device="cuda").manual_seed(i), device=device()).to(t))[1:]
+                     if start == 0 else flat[t][start:start + n])
+        at[t] = start + n
+    outs = [torch.full_like(g, 7) for g in grads]
+    assert sum(g.nbytes for g in grads) > 160 << 20
+    norm = block.GradClipper(grads, outs).clip(3.0)
+    _check(grads, outs, norm, 3.0)
+    kept = [g.clone() for g in grads]
+    assert torch.equal(block.GradClipper(kept).clip(3.0), norm)
+    for k, o in zip(kept, outs):
+        assert torch.equal(k, o)
+
+
 def test_extreme_values():
     big = [torch.full((1000,), 1e30, device=device()), torch.full((10,), 1e-30, device=device())]
     outs = [torch.empty_like(g) for g in big]
