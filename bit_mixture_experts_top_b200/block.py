@@ -11,6 +11,7 @@ workspaces are allocated per call from torch's allocator, so calls on several
 streams, and calls captured into several graphs, share nothing.
 """
 import contextlib
+import ctypes
 
 import torch
 
@@ -27,6 +28,10 @@ def _check(t, name, shape, *dtypes):
     if not t.is_contiguous():
         raise ValueError(f"e4b: {name} must be contiguous")
     return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 _HERE = contextlib.nullcontext()
@@ -69,8 +74,11 @@ class RmsNorm:
                 scales = x.new_empty((T,), dtype=torch.float32) if q_format == e4b.E4B_Q8_ROW else \
                     x.new_empty((T, H // 32), dtype=torch.uint8)
             rstd = x.new_empty((T,), dtype=torch.float32) if want_rstd else None
-            e4b.e4b_rmsnorm(x, residual, self.weight, T, H, self.eps, q_format, r if residual is not None else None, y,
-                            q, scales, rstd)
+            # (the tensors are checked: straight to the library, whose call costs a few microseconds in all)
+            e4b._check(e4b.lib().e4b_rmsnorm(
+                x.data_ptr(), _ptr(residual), self.weight.data_ptr(), T, H, self.eps, q_format,
+                None if residual is None else r.data_ptr(), _ptr(y), _ptr(q), _ptr(scales), _ptr(rstd),
+                e4b._stream(None)), "e4b_rmsnorm")
         return y, q, scales, r, rstd
 
     def forward(self, x, residual=None):
@@ -134,32 +142,41 @@ class GluFfn:
         self.gu_bias = None if gu_bias is None else _check(gu_bias, "gu_bias", (2 * self.I,), torch.float32)
         self.dn_bias = None if dn_bias is None else _check(dn_bias, "dn_bias", (self.H,), torch.float32)
         self.index = self.down.get_device()
+        self._ws_bytes = {}                     # workspace sizes by (entry point, tokens)
         with _on(self.index, self.gate_up, self.gu_bias, self.dn_bias):
             self.desc = e4b.make_ffn_desc(self.H, self.I, glu)
         if e4b.e4b_ffn_workspace_bytes(self.desc, 1) == 0:
             raise ValueError("e4b: unsupported feed-forward shape (H and I are multiples of 8, the GLU limit is "
                              "positive)")
 
-    def _run(self, call, nbytes, x, add, out):
+    def _run(self, name, query, x, add, out):
         if x.dim() != 2:
             raise ValueError("e4b: x must be [T, H]")
         T = x.shape[0]
         _check(x, "x", (T, self.H), torch.bfloat16)
         if add is not None:
             _check(add, "add", (T, self.H), torch.bfloat16)
+        nbytes = self._ws_bytes.get((name, T))
+        if nbytes is None:
+            nbytes = self._ws_bytes[name, T] = query(self.desc, T)
+            if nbytes == 0:
+                raise ValueError(f"e4b: {T} tokens are not supported")
         with _on(self.index, x, add, out):
             out = torch.empty_like(x) if out is None else _check(out, "out", (T, self.H), torch.bfloat16)
-            ws = x.new_empty(nbytes(self.desc, T), dtype=torch.uint8)
-            call(self.desc, T, x, self.gate_up, self.down, self.gu_bias, self.dn_bias, add, out, ws)
+            ws = x.new_empty(nbytes, dtype=torch.uint8)
+            e4b._check(getattr(e4b.lib(), name)(
+                ctypes.byref(self.desc), T, x.data_ptr(), self.gate_up.data_ptr(), self.down.data_ptr(),
+                _ptr(self.gu_bias), _ptr(self.dn_bias), _ptr(add), out.data_ptr(), ws.data_ptr(), nbytes,
+                e4b._stream(None)), name)
         return out, ws
 
     def forward(self, x, add=None, out=None):
         """out [T, H] bf16; add [T, H] bf16 is added to it (the routed experts' output), and out may be add."""
-        return self._run(e4b.e4b_ffn_forward, e4b.e4b_ffn_workspace_bytes, x, add, out)[0]
+        return self._run("e4b_ffn_forward", e4b.e4b_ffn_workspace_bytes, x, add, out)[0]
 
     def forward_train(self, x, add=None, out=None):
         """(out, saved): the forward, and what :meth:`backward` needs of it."""
-        out, ws = self._run(e4b.e4b_ffn_forward_train, e4b.e4b_ffn_train_workspace_bytes, x, add, out)
+        out, ws = self._run("e4b_ffn_forward_train", e4b.e4b_ffn_train_workspace_bytes, x, add, out)
         return out, FfnSaved(x, ws)
 
     def backward(self, saved, dout, weights=True):
@@ -191,6 +208,7 @@ class GradClipper:
         if not tensors:
             raise ValueError("e4b: no gradient tensors")
         self.index = tensors[0].get_device()
+        self._table = ctypes.cast(self.grads, ctypes.c_void_p)
         with _on(self.index, *tensors):
             self.ws_bytes = e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads))
 
@@ -201,5 +219,6 @@ class GradClipper:
             first = self.grads.tensors[0][0]
             norm = first.new_empty((), dtype=torch.float32)
             ws = first.new_empty(self.ws_bytes, dtype=torch.uint8)
-            e4b.e4b_clip_grad_norm(self.grads, float(max_norm), norm, ws)
+            e4b._check(e4b.lib().e4b_clip_grad_norm(self._table, len(self.grads), max_norm, norm.data_ptr(), ws.data_ptr(),
+                                                    self.ws_bytes, e4b._stream(None)), "e4b_clip_grad_norm")
         return norm

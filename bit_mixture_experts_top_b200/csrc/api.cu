@@ -652,7 +652,7 @@ static FfnLayout ffn_layout(const e4b_ffn_desc& d, int32_t T) {
   L.g = take(t * 2 * I * 4);
   L.dG = take(t * 2 * I * 2);
   L.gu_sums = take(dense_colsum_rows(T) * 2 * I * 4);
-  L.dn_sums = take(static_cast<size_t>(column_sum_bf16_blocks(T)) * d.H * 4);
+  L.dn_sums = take(static_cast<size_t>(column_sum_splits(T)) * d.H * 4);
   L.total = o;
   return L;
 }
@@ -802,47 +802,44 @@ e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x,
     st = launch_dense_gemm(g, s);
     if (st != E4B_OK) return st;
   }
+  DenseGemmLaunch rest[3];                           // the products that follow do not depend on one another
+  int n = 0;
   base.epi = kEpiLinear;
-  if (dx) {                                          // dx = dG W_gu
-    DenseGemmLaunch g = base;
+  base.b_mn = true;
+  if (dx) {                                          // dG W_gu
+    DenseGemmLaunch& g = rest[n++] = base;
     g.M = T;
     g.N = d->H;
     g.K = 2 * d->I;
     g.a = dG;
     g.b = w_gu;
-    g.b_mn = true;
     g.out = dx;
-    g.b_early = 1;
-    st = launch_dense_gemm(g, s);
-    if (st != E4B_OK) return st;
+    g.b_early = 1;                                   // (dx comes right after dG)
   }
-  base.a_mn = base.b_mn = true;                      // both contract the tokens
+  base.a_mn = true;                                  // both weight gradients contract the tokens
   base.K = T;
   if (dw_gu) {                                       // dG^T x
-    DenseGemmLaunch g = base;
+    DenseGemmLaunch& g = rest[n++] = base;
     g.M = 2 * d->I;
     g.N = d->H;
     g.a = dG;
     g.b = x;
     g.out = dw_gu;
-    st = launch_dense_gemm(g, s);
-    if (st != E4B_OK) return st;
   }
   if (dw_dn) {                                       // dout^T h
-    DenseGemmLaunch g = base;
+    DenseGemmLaunch& g = rest[n++] = base;
     g.M = d->H;
     g.N = d->I;
     g.a = dout;
     g.b = at<uint16_t>(ws, L.h);
     g.out = dw_dn;
-    st = launch_dense_gemm(g, s);
-    if (st != E4B_OK) return st;
   }
-  if (dgu_bias && launch_column_sum(at<float>(ws, L.gu_sums), sum_rows, 2 * d->I, dgu_bias, s) != cudaSuccess)
-    return E4B_ERR_CUDA;
-  if (ddn_bias && launch_column_sum_bf16(dout, T, d->H, at<float>(ws, L.dn_sums), ddn_bias, s) != cudaSuccess)
-    return E4B_ERR_CUDA;
-  return E4B_OK;
+  if (n > 0) st = launch_dense_group(rest, n, s);
+  if (st != E4B_OK) return st;
+  return launch_column_sums(at<float>(ws, L.gu_sums), sum_rows, 2 * d->I, dgu_bias, dout, T, d->H,
+                            at<float>(ws, L.dn_sums), ddn_bias, s) == cudaSuccess
+             ? E4B_OK
+             : E4B_ERR_CUDA;
 }
 
 static const int32_t kMaxGradTensors = 65536;

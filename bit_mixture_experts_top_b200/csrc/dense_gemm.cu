@@ -773,6 +773,205 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
   }
 }
 
+// ---------------------------------------------------------------------- several products in one launch
+
+// The backward's last three products (dx and both weight gradients) depend on
+// dG alone.  Where each is too small to fill the device, one launch runs them
+// together on 128 x 128 tiles: the tiles of all products, in order, are dealt by
+// their cost (K steps and a fixed part) so that every CTA gets an equal share of
+// the whole.  Operand orders are per product, so the descriptors are chosen at
+// run time; the epilogue is the plain bf16 store.
+constexpr int kMultiMax = 3;
+constexpr int kTileFixed = 3;            // a tile's cost beside its K steps, in steps
+
+struct MultiProblem {
+  int32_t M, N, K, n_tiles, tiles, a_mn, b_mn, wide;
+  uint16_t* out;
+};
+
+struct MultiParams {
+  int32_t count;
+  int32_t* status;
+  uint64_t wait_limit_ns;
+  MultiProblem p[kMultiMax];
+};
+
+struct alignas(64) MultiMaps {
+  CUtensorMap a[kMultiMax], b[kMultiMax];
+};
+
+// Calls body(problem index, tile) for this CTA's tiles, in order, while it returns true.
+template <typename Body>
+__device__ __forceinline__ void walk_tiles(const MultiParams& mp, const Body& body) {
+  int64_t total = 0;
+  auto cost = [&](int i) { return static_cast<int64_t>((mp.p[i].K + BK - 1) / BK + kTileFixed); };
+  for (int i = 0; i < mp.count; ++i) total += mp.p[i].tiles * cost(i);
+  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  int64_t at = 0;                          // cost of the products before
+  for (int i = 0; i < mp.count; ++i) {
+    const int64_t c = cost(i);
+    // tiles whose middle lies in [lo, hi)
+    auto first = [&](int64_t x) {
+      const int64_t d = x - at - c / 2;
+      const int64_t t = d <= 0 ? 0 : (d + c - 1) / c;
+      return static_cast<int>(t < mp.p[i].tiles ? t : mp.p[i].tiles);
+    };
+    const int t1 = first(hi);
+    for (int t = first(lo); t < t1; ++t)
+      if (!body(i, t)) return;
+    at += mp.p[i].tiles * c;
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    dense_multi_kernel(const __grid_constant__ MultiMaps maps, const __grid_constant__ MultiParams mp) {
+  using C = Cfg<128, 1>;
+  constexpr int BN = 128;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  int32_t* s_abort = reinterpret_cast<int32_t*>(smem + C::OFF_MISC + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], EPI_WARPS);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == WARP_MMA) {
+    tmem_alloc(s_tmem, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *s_tmem;
+  const WaitCtx wctx{s_abort, mp.status, mp.wait_limit_ns};
+
+  if (warp == WARP_TMA) {
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, par = 0;
+    bool ok = true;
+    walk_tiles(mp, [&](int i, int tile) {
+      const MultiProblem& q = mp.p[i];
+      const int m0 = tile / q.n_tiles * BM, n0 = tile % q.n_tiles * BN;
+      const int ksteps = (q.K + BK - 1) / BK;
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, int mn, int row0, int k0) {
+        if (mn) {
+          tma_load_2d(dst, map, &full[stage], row0, k0);
+          tma_load_2d(dst + 8192, map, &full[stage], row0 + 64, k0);
+        } else {
+          tma_load_2d(dst, map, &full[stage], k0, row0);
+        }
+      };
+      for (int ks = 0; ks < ksteps; ++ks) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wctx, 1601)) { ok = false; break; }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+          uint8_t* a = smem + stage * C::STAGE_BYTES;
+          load(a, &maps.a[i], q.a_mn, m0, ks * BK);
+          load(a + C::A_BYTES, &maps.b[i], q.b_mn, n0, ks * BK);
+        }
+        __syncwarp();
+        armed |= 1u << stage;
+        par = (par & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+      }
+      return ok;
+    });
+    if (!ok && lane == 0) {
+      for (int s = 0; s < C::STAGES; ++s)
+        if (armed & (1u << s)) mbar_drain(&full[s], (par >> s) & 1u, kDrainNs);
+    }
+  } else if (warp == WARP_MMA) {
+    const uint32_t base = smem_u32(smem);
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    walk_tiles(mp, [&](int i, int) {
+      const MultiProblem& q = mp.p[i];
+      const uint32_t idesc = idesc_bf16_f32(BM, BN) | (q.a_mn ? 1u << 15 : 0u) | (q.b_mn ? 1u << 16 : 0u);
+      const uint64_t da0 = q.a_mn ? smem_desc_mn_sw128(base) : smem_desc_sw128(base);
+      const uint64_t db0 = q.b_mn ? smem_desc_mn_sw128(base + C::A_BYTES) : smem_desc_sw128(base + C::A_BYTES);
+      const uint32_t a_step = (q.a_mn ? 2048 : 32) >> 4, b_step = (q.b_mn ? 2048 : 32) >> 4;
+      const int ksteps = (q.K + BK - 1) / BK, buf = it & 1;
+      if (!mbar_wait_warp(&acc_empty[buf], ((it >> 1) & 1) ^ 1u, wctx, 1602)) ok = false;
+      tc_fence_after_sync();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+      for (int ks = 0; ok && ks < ksteps; ++ks) {
+        if (!mbar_wait_warp(&full[stage], phase, wctx, 1603)) { ok = false; break; }
+        const uint64_t da = da0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+        const uint64_t db = db0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            umma_bf16_ss(d, da + kk * a_step, db + kk * b_step, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&empty[stage]);
+          if (ks == ksteps - 1) umma_commit(&acc_full[buf]);
+        }
+        __syncwarp();
+        issued = true;
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+      }
+      ++it;
+      return ok;
+    });
+    if (!ok && issued && lane == 0)
+      mbar_drain(&empty[stage == 0 ? C::STAGES - 1 : stage - 1], stage == 0 ? phase ^ 1u : phase, kDrainNs);
+  } else if (warp >= WARP_EPI0) {
+    const int q4 = warp & 3, part = (warp - WARP_EPI0) >> 2;
+    int it = 0;
+    walk_tiles(mp, [&](int i, int tile) {
+      const MultiProblem& q = mp.p[i];
+      const int m0 = tile / q.n_tiles * BM, n0 = tile % q.n_tiles * BN, buf = it & 1;
+      if (!__all_sync(kFull, mbar_wait_sleep(&acc_full[buf], (it >> 1) & 1, wctx, 1604, 64))) return false;
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16) + static_cast<uint32_t>(buf * BN);
+      const int row = m0 + 32 * q4 + lane;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c0 = 16 * part + 64 * h, col = n0 + c0;
+        if (col >= q.N) break;
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(taddr + c0, r);
+        tmem_ld_wait();
+        if (row < q.M) {
+          const bool both = col + 8 < q.N;
+          float f[8], g[8];
+          take8(r, 0, f);
+          take8(r, 8, g);
+          const uint4 v[2] = {pack8(f), pack8(g)};
+          store16(q.out + static_cast<int64_t>(row) * q.N + col, v, both, q.wide);
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      ++it;
+      return true;
+    });
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
 // ---------------------------------------------------------------------- host side
 
 // Tensor maps of both operands.  K-contiguous: [rows, K], boxes of 64 K x tile rows; M/N-contiguous:
@@ -886,8 +1085,14 @@ e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
 // width that fills the last wave of pairs may win over 256.  A step of a
 // 128 x 128 tile of one CTA costs 0.8 (issue-bound, whatever its width), a 128-K
 // step of the split kernel 1.7 (it waits for its loads) and its exchange about 6.
+struct Choice {
+  int width;        // of pair tiles; 0: 128 x 128 tiles of one CTA
+  int split;        // > 1: the split kernel with clusters of this size
+  double time;
+};
+
 template <bool A_MN, bool B_MN, int EPI>
-e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
+Choice choose(const DenseGemmLaunch& g) {
   const int64_t sms = device_sm_count();
   auto tiles = [&](int rows, int cols) {
     const int nt = EPI == kEpiGateUp ? cols / 2 : cols;
@@ -895,28 +1100,26 @@ e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
   };
   auto waves = [](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
   const int64_t k64 = (g.K + BK - 1) / BK, k128 = (g.K + 127) / 128, t128 = tiles(128, 128);
-  int width = 256;
-  double pair = waves(tiles(256, 256), sms / 2) * k64 + 4.0;
+  Choice c{256, 1, waves(tiles(256, 256), sms / 2) * k64 + 4.0};
   for (int w = 224; w >= 160; w -= 32) {
     const double t = waves(tiles(256, w), sms / 2) * k64 * (0.1 + 0.9 * w / 256.0) + 4.0;
-    if (t < 0.97 * pair) {
-      pair = t;
-      width = w;
-    }
+    if (t < 0.97 * c.time) c = Choice{w, 1, t};
   }
   const double single = waves(t128, sms) * k64 * 0.8;
-  double best = pair < single ? pair : single;
-  int S = 1;
+  if (single <= c.time) c = Choice{0, 1, single};
   for (int n = 2; n <= 8 && n <= k128 && t128 * n <= sms; ++n) {
     const double t = static_cast<double>((k128 + n - 1) / n) * 1.7 + 6.0;
-    if (t < best && t128 <= split_slots<A_MN, B_MN, EPI>(n)) {
-      best = t;
-      S = n;
-    }
+    if (t < c.time && t128 <= split_slots<A_MN, B_MN, EPI>(n)) c = Choice{0, n, t};
   }
-  if (S > 1) return launch_split<A_MN, B_MN, EPI>(g, S, s);
+  return c;
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
+  const Choice c = choose<A_MN, B_MN, EPI>(g);
+  if (c.split > 1) return launch_split<A_MN, B_MN, EPI>(g, c.split, s);
   if (g.colsum_rows) *g.colsum_rows = (g.M + 31) / 32;
-  if (pair < single) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, width, s);
+  if (c.width) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, c.width, s);
   return launch_typed<128, 1, A_MN, B_MN, EPI>(g, 128, s);
 }
 
@@ -932,6 +1135,64 @@ e4b_status launch_dense_gemm(const DenseGemmLaunch& g, cudaStream_t s) {
       if (!g.a_mn && !g.b_mn) return launch_width<false, false, kEpiLinear>(g, s);
   }
   return E4B_ERR_UNSUPPORTED;
+}
+
+// Plain linear products (no bias, no addition) that depend on earlier launches only: in one launch where the shared
+// tiles take less than the launches one by one (each of which costs about 8 units of its own), else in order.
+e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, cudaStream_t s) {
+  const int64_t sms = device_sm_count();
+  MultiParams mp = {};
+  MultiMaps maps;
+  double apart = 0.0, whole = 0.0, longest = 0.0;
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i) {
+    const Choice c = g[i].a_mn ? choose<true, true, kEpiLinear>(g[i])
+                     : g[i].b_mn ? choose<false, true, kEpiLinear>(g[i]) : choose<false, false, kEpiLinear>(g[i]);
+    apart += c.time + 8.0;
+    MultiProblem& q = mp.p[i];
+    q.M = g[i].M;
+    q.N = g[i].N;
+    q.K = g[i].K;
+    q.n_tiles = (g[i].N + 127) / 128;
+    const int64_t t = (static_cast<int64_t>(g[i].M) + BM - 1) / BM * q.n_tiles;
+    q.tiles = static_cast<int32_t>(t);
+    q.a_mn = g[i].a_mn;
+    q.b_mn = g[i].b_mn;
+    q.out = g[i].out;
+    q.wide = g[i].N % 16 == 0 && aligned(g[i].out, 32) ? 1 : 0;
+    const double one = 0.8 * ((g[i].K + BK - 1) / BK + kTileFixed);
+    whole += one * static_cast<double>(t) / static_cast<double>(sms);
+    if (one > longest) longest = one;
+    tiles += t;
+  }
+  const double together = (whole > longest ? whole : longest) + 0.5 * longest + 8.0;
+  if (count < 2 || count > kMultiMax || together >= apart) {
+    for (int i = 0; i < count; ++i) {
+      const e4b_status st = launch_dense_gemm(g[i], s);
+      if (st != E4B_OK) return st;
+    }
+    return E4B_OK;
+  }
+  for (int i = 0; i < count; ++i) {
+    const bool ok = g[i].a_mn ? encode_operands<true, true, kEpiLinear>(g[i], 128, &maps.a[i], &maps.b[i])
+                    : g[i].b_mn ? encode_operands<false, true, kEpiLinear>(g[i], 128, &maps.a[i], &maps.b[i])
+                                : encode_operands<false, false, kEpiLinear>(g[i], 128, &maps.a[i], &maps.b[i]);
+    if (!ok) return E4B_ERR_CUDA;
+  }
+  for (int i = count; i < kMultiMax; ++i) {
+    maps.a[i] = maps.a[0];
+    maps.b[i] = maps.b[0];
+  }
+  mp.count = count;
+  mp.status = g[0].status;
+  mp.wait_limit_ns = kWaitLimitNs;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  if (allow_smem(dense_multi_kernel, Cfg<128, 1>::SMEM_BYTES, once, attr_err) != cudaSuccess) return E4B_ERR_CUDA;
+  return launch_pdl(dense_multi_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(THREADS),
+                    Cfg<128, 1>::SMEM_BYTES, s, maps, mp) == cudaSuccess
+             ? E4B_OK
+             : E4B_ERR_CUDA;
 }
 
 }  // namespace e4b

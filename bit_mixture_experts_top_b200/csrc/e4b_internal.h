@@ -214,9 +214,11 @@ cudaError_t launch_rmsnorm_backward(const NormBackwardLaunch& p, cudaStream_t s)
 
 // out[n] = sum over rows of in[., n] (fp32, fixed order).
 cudaError_t launch_column_sum(const float* in, int rows, int N, float* out, cudaStream_t s);
-// The same of bf16 rows (N even, 4-byte aligned); partial: [column_sum_bf16_blocks(rows), N] fp32, 8-byte aligned.
-int column_sum_bf16_blocks(int rows);
-cudaError_t launch_column_sum_bf16(const uint16_t* in, int rows, int N, float* partial, float* out, cudaStream_t s);
+// Two of them in one launch, either left out by a null `out`: of the fp32 rows a, and of the bf16 rows b (Nb even,
+// 4-byte aligned).  partial: [column_sum_splits(rows_b), Nb] fp32, 8-byte aligned.
+int column_sum_splits(int rows);
+cudaError_t launch_column_sums(const float* a, int rows_a, int Na, float* out_a, const uint16_t* b, int rows_b, int Nb,
+                               float* partial, float* out_b, cudaStream_t s);
 
 // Gradient norm and clipping; partial holds grad_norm_partials(tensors) doubles.
 size_t grad_norm_partials(int32_t tensors);
@@ -247,6 +249,8 @@ struct DenseGemmLaunch {
 };
 inline size_t dense_colsum_rows(int32_t M) { return (static_cast<size_t>(M) + 127) / 128 * 8; }
 e4b_status launch_dense_gemm(const DenseGemmLaunch& g, cudaStream_t s);
+// Up to three kEpiLinear products without bias or addition that do not depend on one another.
+e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, cudaStream_t s);
 
 // The same products for at most 32 tokens, bound by the weight stream (dense_decode_takes says for which).  The down
 // launch (gate_up false) has to follow the gate_up launch that writes its x directly on the stream.
