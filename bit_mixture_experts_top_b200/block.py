@@ -3,8 +3,9 @@
 Thin owners of device buffers around the C ABI, as :mod:`layer` is for the
 routed layer: :class:`RmsNorm` (the layer's input from the hidden stream, and
 its backward), :class:`GluFfn` (the shared expert that runs next to the routed
-ones, forward and backward) and :class:`GradClipper` (the gradients that the backward calls
-leave).  Nothing here computes.
+ones, forward and backward), :class:`MoeBlock` (norm, router, routed layer and
+shared expert in their order, forward and backward) and :class:`GradClipper`
+(the gradients that the backward calls leave).  Nothing here computes.
 
 Every call runs on the current stream of the tensors' device.  Outputs and
 workspaces are allocated per call from torch's allocator, so calls on several
@@ -119,8 +120,9 @@ class RmsNorm:
 
 
 class FfnSaved:
-    """What :meth:`GluFfn.forward_train` keeps for one :meth:`GluFfn.backward`: the input and the workspace with the
-    pre-activations and h."""
+    """What :meth:`GluFfn.forward_train` keeps for :meth:`GluFfn.backward`: the input (not copied: it must not change
+    before the backward) and the workspace with the pre-activations and h, whose scratch one backward at a time
+    uses."""
 
     def __init__(self, x, ws):
         self.x, self.ws = x, ws
@@ -194,6 +196,55 @@ class GluFfn:
                 if weights and self.dn_bias is not None else None
             e4b.e4b_ffn_backward(self.desc, T, saved.x, dout, self.gate_up, self.down, dx, dgu, ddn, dbg, dbd, saved.ws)
         return dx, dgu, ddn, dbg, dbd
+
+
+class MoeBlock:
+    """The feed-forward half of a block: norm, router, routed 4-bit layer and, where there is one, the shared expert.
+
+    norm: :class:`RmsNorm`; moe: :class:`layer.MoeLayer`; shared: :class:`GluFfn` or None; router: a callable
+    y [T, H] -> logits [T, E] (bf16), the model's own projection of the normed rows."""
+
+    def __init__(self, norm, router, moe, shared=None):
+        if moe.H != norm.H or (shared is not None and shared.H != norm.H):
+            raise ValueError("e4b: the norm, the routed layer and the shared expert differ in H")
+        self.norm, self.router, self.moe, self.shared = norm, router, moe, shared
+
+    def _logits(self, y):
+        return _check(self.router(y), "logits", (y.shape[0], self.moe.E), torch.bfloat16)
+
+    def forward(self, x, residual=None):
+        """(out [T, H], r [T, H]): the experts' output and the stream x + residual that it is added to next."""
+        y, r = self.norm.forward(x, residual)
+        out = self.moe.forward(y, self._logits(y))
+        return (out if self.shared is None else self.shared.forward(y, add=out, out=out)), r
+
+    def forward_train(self, x, residual=None):
+        """(out, r, saved): the forward with what :meth:`backward` needs.  The routed layer keeps its part in its own
+        workspace, so each forward_train is followed by its backward before the next."""
+        y, r, rstd = self.norm.forward_train(x, residual)
+        logits = self._logits(y)
+        out = self.moe.forward_train(y, logits)
+        kept = None
+        if self.shared is not None:
+            out, kept = self.shared.forward_train(y, add=out, out=out)
+        return out, r, (y, r, rstd, logits, kept)
+
+    def backward(self, saved, dout, dr=None, router_grad=None, weights=True):
+        """Gradients of sum(dout * out) + sum(dr * r) as a dict: dx [T, H] bf16 (of x and residual alike), norm [H]
+        fp32, dlogits [T, E] fp32, lora_A / lora_B fp32 (None without LoRA) and, with a shared expert, gate_up, down,
+        gu_bias and dn_bias (None where frozen or absent).  router_grad: a callable dlogits -> its part of dy [T, H],
+        the router's own backward; None leaves the router's path out of dx."""
+        y, r, rstd, logits, kept = saved
+        dy, dlogits, dA, dB = self.moe.backward(logits, dout)
+        got = dict(dlogits=dlogits, lora_A=dA, lora_B=dB)
+        if self.shared is not None:
+            dys, *rest = self.shared.backward(kept, dout, weights)
+            got.update(zip(("gate_up", "down", "gu_bias", "dn_bias"), rest))
+            dy += dys
+        if router_grad is not None:
+            dy += router_grad(dlogits)
+        got["dx"], got["norm"] = self.norm.backward(dy, r, rstd, dr)
+        return got
 
 
 class GradClipper:

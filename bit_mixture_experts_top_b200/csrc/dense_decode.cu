@@ -24,8 +24,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
 
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(32 * WARPS) dense_decode_kernel(const DenseDec
         p.g_out[2 * static_cast<int64_t>(tok) * p.N + n] = a;
         p.g_out[2 * static_cast<int64_t>(tok) * p.N + p.N + n] = b;
       }
-      a = expert_act(p.ep, a, b);
+      a = dense_act(p.ep, a, b);
     } else {
       if (p.bias) a += __ldg(p.bias + n);
       if (p.add) a += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.add)[at]);
@@ -193,12 +191,9 @@ template <int NB, int STAGES, bool GATE_UP>
 cudaError_t launch_typed(const DenseDecodeLaunch& p, int grid, cudaStream_t s) {
   auto kern = dense_decode_kernel<NB, STAGES, GATE_UP>;
   constexpr int smem = smem_bytes<NB, STAGES>();
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kern, smem, allowed);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(grid), dim3(32 * WARPS), smem, s, p);
 }
 

@@ -24,9 +24,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-#include <mutex>
-
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
 
@@ -134,12 +131,12 @@ __device__ __forceinline__ void store16(uint16_t* o, const uint4 (&v)[2], bool b
 // d(act)/d(gate) and d(act)/d(up); the clamps pass the gradient inside their range, ends included.
 __device__ __forceinline__ void act_grads(const Params& p, float gate, float up, float& dg, float& du) {
   if (p.act == E4B_ACT_CLAMPED_GLU) {
-    const float g = fminf(gate, p.limit);
-    const float u = fminf(fmaxf(up, -p.limit), p.limit);
+    const float g = clamp_up(gate, p.limit);
+    const float u = -clamp_up(-clamp_up(up, p.limit), p.limit);
     const float s = __fdividef(1.0f, 1.0f + __expf(-p.alpha * g));
     const float df = s * (1.0f + p.alpha * g * (1.0f - s));
-    dg = gate <= p.limit ? df * (u + p.beta) : 0.0f;
-    du = (up >= -p.limit && up <= p.limit) ? g * s : 0.0f;
+    dg = gate > p.limit ? 0.0f : df * (u + p.beta);
+    du = (up < -p.limit || up > p.limit) ? 0.0f : g * s;
     return;
   }
   const float s = __fdividef(1.0f, 1.0f + __expf(-gate));
@@ -211,7 +208,7 @@ __device__ __forceinline__ uint4 finish_gate_up(const Params& p, int row, bool r
   }
   const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = expert_act(ep, g[i], u[i]);
+  for (int i = 0; i < 8; ++i) g[i] = dense_act(ep, g[i], u[i]);
   return pack8(g);
 }
 
@@ -717,10 +714,10 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
         u.w = __shfl_down_sync(kFull, f.w, 16);
         if (lane < 16 && col_in) {
           const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
-          f.x = expert_act(ep, f.x, u.x);
-          f.y = expert_act(ep, f.y, u.y);
-          f.z = expert_act(ep, f.z, u.z);
-          f.w = expert_act(ep, f.w, u.w);
+          f.x = dense_act(ep, f.x, u.x);
+          f.y = dense_act(ep, f.y, u.y);
+          f.z = dense_act(ep, f.z, u.z);
+          f.w = dense_act(ep, f.w, u.w);
           *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
         }
       } else if constexpr (EPI == kEpiLinear) {
@@ -1013,19 +1010,12 @@ Params make_params(const DenseGemmLaunch& g, int tile_rows, int width, int tile_
   return p;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes, std::once_flag& once, cudaError_t& err) {
-  std::call_once(once, [&] { err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
-  return err;
-}
-
 template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
 e4b_status launch_typed(const DenseGemmLaunch& g, int width, cudaStream_t s) {
   using C = Cfg<BN, CG>;
   auto kern = dense_gemm_kernel<BN, CG, A_MN, B_MN, EPI>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  if (allow_smem(kern, C::SMEM_BYTES, once, attr_err) != cudaSuccess) return E4B_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem(kern, C::SMEM_BYTES, allowed) != cudaSuccess) return E4B_ERR_CUDA;
   const int NT = EPI == kEpiGateUp ? width / 2 : width;
   CUtensorMap ta, tb;
   if (!encode_operands<A_MN, B_MN, EPI>(g, EPI == kEpiGateUp ? NT : width / CG, &ta, &tb)) return E4B_ERR_CUDA;
@@ -1043,9 +1033,8 @@ template <bool A_MN, bool B_MN, int EPI>
 int split_slots(int S) {
   using C = SplitCfg;
   auto kern = dense_split_kernel<A_MN, B_MN, EPI>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  if (allow_smem(kern, C::SMEM_BYTES, once, attr_err) != cudaSuccess) return 0;
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem(kern, C::SMEM_BYTES, allowed) != cudaSuccess) return 0;
   static std::atomic<int> cache[16][9];                 // + 1, so that 0 is "not asked yet"
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
@@ -1186,9 +1175,8 @@ e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, cudaStream_t 
   mp.count = count;
   mp.status = g[0].status;
   mp.wait_limit_ns = kWaitLimitNs;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  if (allow_smem(dense_multi_kernel, Cfg<128, 1>::SMEM_BYTES, once, attr_err) != cudaSuccess) return E4B_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem(dense_multi_kernel, Cfg<128, 1>::SMEM_BYTES, allowed) != cudaSuccess) return E4B_ERR_CUDA;
   return launch_pdl(dense_multi_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(THREADS),
                     Cfg<128, 1>::SMEM_BYTES, s, maps, mp) == cudaSuccess
              ? E4B_OK

@@ -413,4 +413,16 @@ __device__ __forceinline__ float expert_act(const Epilogue& ep, float gate, floa
   return __fdividef(gate, 1.0f + __expf(-gate)) * up;
 }
 
+// The same activations for the dense block, with clamps that let a NaN through.
+__device__ __forceinline__ float clamp_up(float v, float limit) { return v > limit ? limit : v; }
+
+__device__ __forceinline__ float dense_act(const Epilogue& ep, float gate, float up) {
+  if (ep.glu == E4B_ACT_CLAMPED_GLU) {
+    const float g = clamp_up(gate, ep.limit);
+    const float u = -clamp_up(-clamp_up(up, ep.limit), ep.limit);
+    return __fdividef(g, 1.0f + __expf(-ep.alpha * g)) * (u + ep.beta);
+  }
+  return __fdividef(gate, 1.0f + __expf(-gate)) * up;
+}
+
 }  // namespace e4b

@@ -25,8 +25,6 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "e4b_device.cuh"
 #include "e4b_internal.h"
 
@@ -591,12 +589,9 @@ int threads_for(int H, int vpt) {
 template <typename DY, int VPT, int STAGES>
 cudaError_t launch_backward_vec(const NormBackwardLaunch& p, int blocks, cudaStream_t s) {
   auto kern = norm_backward_kernel<DY, VPT, STAGES>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kern, kSlotBytes, allowed);
+  if (e != cudaSuccess) return e;
   // as many groups as threads, barriers and shared memory allow; their weight gradients (4 H bytes each) reuse
   // the slots, which are never smaller
   const int tx = threads_for(p.H, VPT), group = STAGES * (static_cast<int>(sizeof(DY)) + (p.dr ? 4 : 2)) * p.H;

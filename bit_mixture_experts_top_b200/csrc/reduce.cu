@@ -11,7 +11,7 @@
 namespace e4b {
 namespace {
 
-constexpr int kGroups = 16;   // row groups per block: one warp each
+constexpr int kGroups = 32;   // row groups per block: one warp each, so that a few hundred rows are one round of loads
 
 // 32 columns of fp32 rows [rows, N].
 __device__ __forceinline__ void sum_f32(const float* __restrict__ in, int rows, int N, float* __restrict__ out,
@@ -39,7 +39,7 @@ __device__ __forceinline__ void sum_bf16(const uint32_t* __restrict__ in, int r0
   const int c = block * 32 + lane;
   float2 s = make_float2(0.0f, 0.0f);
   if (2 * c < N) {
-#pragma unroll 8
+#pragma unroll 16
     for (int r = r0 + g; r < r1; r += kGroups) {
       const uint32_t v = in[static_cast<int64_t>(r) * (N >> 1) + c];
       s.x += __uint_as_float(v << 16);
@@ -92,7 +92,7 @@ cudaError_t launch_column_sum(const float* in, int rows, int N, float* out, cuda
   return launch_pdl(column_sum_kernel, dim3((N + 31) / 32), dim3(32 * kGroups), 0, s, in, rows, N, out);
 }
 
-// One share up to 1024 rows (64 per warp), then as many as keep that.
+// One share up to 1024 rows (32 per warp), then as many as keep that.
 int column_sum_splits(int rows) {
   const int b = (rows + 1023) / 1024;
   return b < 1 ? 1 : (b > 128 ? 128 : b);

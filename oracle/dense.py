@@ -107,7 +107,7 @@ def act_grads(g, u, glu=None):
     gc, uc = np.minimum(g, limit), np.clip(u, -limit, limit)
     s = 1.0 / (1.0 + np.exp(-alpha * gc))
     dg = (s + alpha * gc * s * (1.0 - s)) * (uc + beta)
-    return np.where(g <= limit, dg, 0.0), np.where((u >= -limit) & (u <= limit), gc * s, 0.0)
+    return np.where(g > limit, 0.0, dg), np.where((u < -limit) | (u > limit), 0.0, gc * s)
 
 
 def ffn(x, w_gu, w_dn, gu_bias=None, dn_bias=None, add=None, glu=None):

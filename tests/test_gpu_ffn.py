@@ -213,6 +213,30 @@ def test_graphs_share_nothing_and_read_new_inputs(T):
     assert torch.equal(outs[0][0], want)
 
 
+@pytest.mark.parametrize("T", [5, 40, 700])
+@pytest.mark.parametrize("glu", [None, GLU])
+def test_large_pre_activations_and_values_that_are_not_finite(T, glu):
+    # gates of +-several hundred saturate the sigmoid; a NaN or an infinity of one token stays with that token
+    c = Case(T, 136, 264, glu=glu, wide=60.0)
+    assert np.abs(c.G).max() > 200
+    out, saved = c.ffn.forward_train(c.d["x"])
+    got = bf16_to_f64(out)
+    assert np.isfinite(got).all() and np.linalg.norm(got - c.out) <= 5e-3 * np.linalg.norm(c.out)
+    dx = bf16_to_f64(c.ffn.backward(saved, c.d["dout"])[0])
+    assert np.isfinite(dx).all()
+    x = c.d["x"].clone()
+    x[2, 7], x[4, 100] = float("nan"), float("inf")
+    out2, saved = c.ffn.forward_train(x)
+    keep = [t for t in range(T) if t not in (2, 4)]
+    assert torch.equal(out2[keep], out[keep])
+    assert bool(torch.isnan(out2[2]).all())
+    with np.errstate(all="ignore"):
+        want = dense.ffn(x.double().cpu().numpy(), c.f["gu"], c.f["dn"], glu=glu)[0]
+    assert np.array_equal(np.isnan(bf16_to_f64(out2)), np.isnan(want))
+    dx2 = c.ffn.backward(saved, c.d["dout"])[0]
+    assert torch.equal(dx2[keep], torch.from_numpy(dx).to(device()).bfloat16()[keep]) and bool(torch.isnan(dx2[2]).all())
+
+
 def test_refusals():
     c = Case(20, 64, 128)
     x = c.d["x"]
