@@ -259,7 +259,7 @@ class GradClipper:
         if not tensors:
             raise ValueError("e4b: no gradient tensors")
         self.index = tensors[0].get_device()
-        self._table = ctypes.cast(self.grads, ctypes.c_void_p)
+        self._table = ctypes.addressof(self.grads)
         with _on(self.index, *tensors):
             self.ws_bytes = e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads))
 

@@ -361,7 +361,7 @@ def e4b_clip_grad_norm_workspace_bytes(tensors):
 def e4b_clip_grad_norm(grads, max_norm, total_norm, ws, stream=None):
     """grads: the array of :func:`make_grads`."""
     _need_cuda(total_norm, ws)
-    _check(lib().e4b_clip_grad_norm(ctypes.cast(grads, ctypes.c_void_p), len(grads), max_norm, _ptr(total_norm),
+    _check(lib().e4b_clip_grad_norm(ctypes.addressof(grads), len(grads), max_norm, _ptr(total_norm),
                                     _ptr(ws), ws.nbytes, _stream(stream)), "e4b_clip_grad_norm")
     return total_norm
 

@@ -174,6 +174,23 @@ def test_graph_replay_and_two_clippers_at_once():
     _check(b, ob, nb, 0.5)
 
 
+def test_a_dropped_clipper_lets_its_tensors_go_at_once():
+    import gc
+    import weakref
+    gc.disable()
+    try:
+        g = _grads([100, 7])
+        c = block.GradClipper(g)
+        c.clip(1.0)
+        e4b.e4b_clip_grad_norm(c.grads, 1.0, torch.empty(1, device=device()),
+                               torch.empty(e4b.e4b_clip_grad_norm_workspace_bytes(2), dtype=torch.uint8, device=device()))
+        ref = weakref.ref(g[0])
+        del g, c
+        assert ref() is None
+    finally:
+        gc.enable()
+
+
 def test_refusals():
     g = _grads([100, 100])
     with pytest.raises(RuntimeError, match="INVALID_ARG"):
