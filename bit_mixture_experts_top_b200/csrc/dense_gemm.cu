@@ -227,19 +227,27 @@ __device__ __forceinline__ uint4 finish_linear(const Params& p, int row, bool ro
 }
 
 // All lanes of the warp call it with rows row0 + lane (row0 a multiple of 32).
-__device__ __forceinline__ void finish_dact(const Params& p, int row, bool row_in, int col, int lane,
+// G of eight columns, loaded ahead of its use.
+struct SavedG {
+  float g[8], u[8];
+
+  __device__ __forceinline__ void load(const Params& p, int row, bool in, int col) {
+    if (!in) return;
+    const float* gp = p.g_in + static_cast<int64_t>(row) * 2 * p.N + col;
+    load8f(gp, g);
+    load8f(gp + p.N, u);
+  }
+};
+
+__device__ __forceinline__ void finish_dact(const Params& p, int row, bool row_in, int col, int lane, const SavedG& G,
                                             const float (&dh)[8], uint4& og, uint4& ou) {
   float dg[8], du[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dg[i] = du[i] = 0.0f;
   if (row_in) {
-    float g[8], u[8];
-    const float* gp = p.g_in + static_cast<int64_t>(row) * 2 * p.N + col;
-    load8f(gp, g);
-    load8f(gp + p.N, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      act_grads(p, g[i], u[i], dg[i], du[i]);
+      act_grads(p, G.g[i], G.u[i], dg[i], du[i]);
       dg[i] *= dh[i];
       du[i] *= dh[i];
     }
@@ -435,11 +443,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int c0 = 16 * part; c0 < NT; c0 += 16 * (EPI_WARPS / 4)) {
         const int col = nt * NT + c0;
         if (col >= p.N) break;
+        const bool both = col + 8 < p.N;               // (a tile's width is a multiple of 16)
         uint32_t r[16], u[16];
+        SavedG G[2];
         tmem_ld_32x32b_x16(taddr + c0, r);
         if constexpr (EPI == kEpiGateUp) tmem_ld_32x32b_x16(taddr + NT + c0, u);
+        if constexpr (EPI == kEpiDact) {
+          G[0].load(p, row, row_in, col);
+          G[1].load(p, row, row_in && both, col + 8);
+        }
         tmem_ld_wait();
-        const bool both = col + 8 < p.N;               // (a tile's width is a multiple of 16)
         uint4 v[2], w[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else if constexpr (EPI == kEpiLinear) {
             v[j] = finish_linear(p, row, row_in, col + 8 * j, f);
           } else {
-            finish_dact(p, row, row_in, col + 8 * j, lane, f, v[j], w[j]);
+            finish_dact(p, row, row_in, col + 8 * j, lane, G[j], f, v[j], w[j]);
           }
         }
         if (row_in) {
