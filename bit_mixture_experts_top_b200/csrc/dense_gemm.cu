@@ -498,10 +498,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // A product too small to give every SM a tile: a cluster of S CTAs shares one
 // 128 x 128 tile, each multiplies its part of K, and the partial tiles meet
-// through distributed shared memory: every CTA adds the S parts, in rank order,
-// of its share of the rows (whole rows, a warp each: contiguous 512-byte reads
-// from every rank and contiguous stores; a lane-per-row layout took five times
-// as long) and runs the epilogue on them.  Stages hold 128 of K: with tiles this
+// through distributed shared memory: every CTA adds the S parts, from its own
+// rank on, of its share of the rows (whole rows, a warp each: contiguous 512-byte
+// reads from every rank and contiguous stores; a lane-per-row layout took five
+// times as long) and runs the epilogue on them.  Stages hold 128 of K: with tiles this
 // narrow the per-stage wait, not the MMA, is what costs.
 //
 // B (weights) may be loaded before the previous launch has completed when that
@@ -707,55 +707,70 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
     if (EPI != kEpiDact && p.bias && col_in) bias = bias4(p, EPI == kEpiGateUp && lane >= 16 ? p.N + col : col);
     float4 sg = make_float4(0.f, 0.f, 0.f, 0.f), su = sg;      // dact: column sums over this warp's rows
+    constexpr int GROUP = 2;                       // rows whose parts are on their way together
+    for (int r0 = rank + S * ew; r0 < rows; r0 += GROUP * S * C::EPI) {
+      float4 sum[GROUP];
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) sum[i] = bias;
 #pragma unroll 2
-    for (int r = rank + S * ew; r < rows; r += S * C::EPI) {
-      const int64_t row = m0 + r;
-      float4 f = bias;
-#pragma unroll 4
       for (int s = 0; s < S; ++s) {
         uint32_t at;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine + r * C::PITCH * 4), "r"(s));
-        add4(f, load_cluster(at));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(rank + s < S ? rank + s : rank + s - S));
+        float4 part[GROUP];
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+          const int r = r0 + i * S * C::EPI;
+          part[i] = r < rows ? load_cluster(at + r * C::PITCH * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) add4(sum[i], part[i]);
       }
-      if constexpr (EPI == kEpiGateUp) {               // lanes 0..15 hold gate, 16..31 the matching up features
-        if (p.g_out && col_in)
-          *reinterpret_cast<float4*>(p.g_out + row * 2 * p.N + (lane >= 16 ? p.N : 0) + col) = f;
-        float4 u;
-        u.x = __shfl_down_sync(kFull, f.x, 16);
-        u.y = __shfl_down_sync(kFull, f.y, 16);
-        u.z = __shfl_down_sync(kFull, f.z, 16);
-        u.w = __shfl_down_sync(kFull, f.w, 16);
-        if (lane < 16 && col_in) {
-          const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
-          f.x = dense_act(ep, f.x, u.x);
-          f.y = dense_act(ep, f.y, u.y);
-          f.z = dense_act(ep, f.z, u.z);
-          f.w = dense_act(ep, f.w, u.w);
-          *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
-        }
-      } else if constexpr (EPI == kEpiLinear) {
-        if (col_in) {
-          if (p.add) {
-            const uint2 a = *reinterpret_cast<const uint2*>(p.add + row * p.N + col);
-            add4(f, make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u),
-                                __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xFFFF0000u)));
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        const int r = r0 + i * S * C::EPI;
+        if (r >= rows) break;
+        const int64_t row = m0 + r;
+        float4 f = sum[i];
+        if constexpr (EPI == kEpiGateUp) {             // lanes 0..15 hold gate, 16..31 the matching up features
+          if (p.g_out && col_in)
+            *reinterpret_cast<float4*>(p.g_out + row * 2 * p.N + (lane >= 16 ? p.N : 0) + col) = f;
+          float4 u;
+          u.x = __shfl_down_sync(kFull, f.x, 16);
+          u.y = __shfl_down_sync(kFull, f.y, 16);
+          u.z = __shfl_down_sync(kFull, f.z, 16);
+          u.w = __shfl_down_sync(kFull, f.w, 16);
+          if (lane < 16 && col_in) {
+            const Epilogue ep{nullptr, p.act, p.alpha, p.limit, p.beta};
+            f.x = dense_act(ep, f.x, u.x);
+            f.y = dense_act(ep, f.y, u.y);
+            f.z = dense_act(ep, f.z, u.z);
+            f.w = dense_act(ep, f.w, u.w);
+            *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
           }
-          *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
+        } else if constexpr (EPI == kEpiLinear) {
+          if (col_in) {
+            if (p.add) {
+              const uint2 a = *reinterpret_cast<const uint2*>(p.add + row * p.N + col);
+              add4(f, make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u),
+                                  __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xFFFF0000u)));
+            }
+            *reinterpret_cast<uint2*>(p.out + row * p.N + col) = pack4(f);
+          }
+        } else if (col_in) {
+          const float* gp = p.g_in + row * 2 * p.N + col;
+          const float4 g = *reinterpret_cast<const float4*>(gp), u = *reinterpret_cast<const float4*>(gp + p.N);
+          float4 dg, du;
+          act_grads(p, g.x, u.x, dg.x, du.x);
+          act_grads(p, g.y, u.y, dg.y, du.y);
+          act_grads(p, g.z, u.z, dg.z, du.z);
+          act_grads(p, g.w, u.w, dg.w, du.w);
+          dg = make_float4(dg.x * f.x, dg.y * f.y, dg.z * f.z, dg.w * f.w);
+          du = make_float4(du.x * f.x, du.y * f.y, du.z * f.z, du.w * f.w);
+          *reinterpret_cast<uint2*>(p.out + row * 2 * p.N + col) = pack4(dg);
+          *reinterpret_cast<uint2*>(p.out + row * 2 * p.N + p.N + col) = pack4(du);
+          add4(sg, dg);
+          add4(su, du);
         }
-      } else if (col_in) {
-        const float* gp = p.g_in + row * 2 * p.N + col;
-        const float4 g = *reinterpret_cast<const float4*>(gp), u = *reinterpret_cast<const float4*>(gp + p.N);
-        float4 dg, du;
-        act_grads(p, g.x, u.x, dg.x, du.x);
-        act_grads(p, g.y, u.y, dg.y, du.y);
-        act_grads(p, g.z, u.z, dg.z, du.z);
-        act_grads(p, g.w, u.w, dg.w, du.w);
-        dg = make_float4(dg.x * f.x, dg.y * f.y, dg.z * f.z, dg.w * f.w);
-        du = make_float4(du.x * f.x, du.y * f.y, du.z * f.z, du.w * f.w);
-        *reinterpret_cast<uint2*>(p.out + row * 2 * p.N + col) = pack4(dg);
-        *reinterpret_cast<uint2*>(p.out + row * 2 * p.N + p.N + col) = pack4(du);
-        add4(sg, dg);
-        add4(su, du);
       }
     }
     if constexpr (EPI == kEpiDact) {
