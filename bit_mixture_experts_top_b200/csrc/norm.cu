@@ -62,6 +62,69 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
+// Two products in one instruction, each rounded as a single one.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 c, a, b;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// The larger of m and both magnitudes; a NaN wins (as 0x7FFFFFFF, above infinity when read as an integer).
+__device__ __forceinline__ float max_abs2(float m, float2 v) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v.x)));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v.y)));
+  return m;
+}
+
+// x + residual, each element one exact sum rounded once to bf16.
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&y[i]));
+    r[i] = *reinterpret_cast<const uint32_t*>(&s);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Sum of the eight squares (each exact in fp32), in fp64.
+__device__ __forceinline__ double squares8(const uint4& v, double sum) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = pair_of(w[i]), q = mul2(f, f);
+    sum += static_cast<double>(q.x);
+    sum += static_cast<double>(q.y);
+  }
+  return sum;
+}
+
+// y = fl32(fl32(r * rstd) * w) of eight values, and the largest magnitude with m.
+__device__ __forceinline__ void normed8(const uint4& r, const uint4& w, float rstd, float2 (&y)[4], float& m) {
+  const uint32_t a[4] = {r.x, r.y, r.z, r.w}, b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[i] = mul2(mul2(pair_of(a[i]), make_float2(rstd, rstd)), pair_of(b[i]));
+    m = max_abs2(m, y[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y), pack2(f[2].x, f[2].y), pack2(f[3].x, f[3].y));
+}
+
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
   return static_cast<uint16_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
@@ -117,9 +180,9 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t amax_bits) {
 // 2^(127 - byte) as fp32, exact (a finite block's byte is at most 247).
 __device__ __forceinline__ float mx_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-__device__ __forceinline__ uint2 codes8(const float (&f)[8]) {
-  return make_uint2(e4m3x2(f[0], f[1]) | (static_cast<uint32_t>(e4m3x2(f[2], f[3])) << 16),
-                    e4m3x2(f[4], f[5]) | (static_cast<uint32_t>(e4m3x2(f[6], f[7])) << 16));
+__device__ __forceinline__ uint2 codes8(const float2 (&f)[4]) {
+  return make_uint2(e4m3x2(f[0].x, f[0].y) | (static_cast<uint32_t>(e4m3x2(f[1].x, f[1].y)) << 16),
+                    e4m3x2(f[2].x, f[2].y) | (static_cast<uint32_t>(e4m3x2(f[3].x, f[3].y)) << 16));
 }
 
 // Byte of the 32-value block that four adjacent lanes hold, from each lane's own maximum.
@@ -129,26 +192,28 @@ __device__ __forceinline__ uint32_t block_byte(uint32_t m) {
   return mx_byte(m);
 }
 
-__device__ __forceinline__ uint2 mx_codes(const float (&f)[8], uint32_t byte) {
+__device__ __forceinline__ uint2 mx_codes(const float2 (&f)[4], uint32_t byte) {
   if (byte == 255u) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   const float s = mx_inverse(byte);
-  float v[8];
+  float2 v[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = f[j] * s;
+  for (int j = 0; j < 4; ++j) v[j] = mul2(f[j], make_float2(s, s));
   return codes8(v);
 }
 
-__device__ __forceinline__ uint2 row_codes(const float (&f)[8], float s, uint32_t amax_bits) {
+__device__ __forceinline__ uint2 row_codes(const float2 (&f)[4], float s, uint32_t amax_bits) {
   if (amax_bits >= kInfBits) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   // fl32(f / s) by Markstein's correction of f * RN(1/s), as in the NF4 quantiser; a tiny scale is lifted
   // with its values by 2^96 so that the residual stays normal (quotients that underflow have code 0 anyway)
   const float up = s < 0x1p-60f ? 0x1p96f : 1.0f;
   const float a = s * up, r = __frcp_rn(a);
-  float v[8];
+  float2 v[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = f[j] * up, q = x * r;
-    v[j] = copysignf(fmaf(fmaf(-a, q, x), r, q), x);   // (the correction would turn -0 into 0)
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = mul2(f[j], make_float2(up, up)), q = mul2(x, make_float2(r, r));
+    // (the correction would turn -0 into 0)
+    v[j].x = copysignf(fmaf(fmaf(-a, q.x, x.x), r, q.x), x.x);
+    v[j].y = copysignf(fmaf(fmaf(-a, q.y, x.y), r, q.y), x.y);
   }
   return codes8(v);
 }
@@ -170,8 +235,8 @@ __device__ __forceinline__ float rstd_of(double sum, double inv_h, double eps) {
 // ---------------------------------------------------------------------- forward
 
 // One block per row, VPT vectors of eight values per thread.
-template <int VPT>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch p) {
+template <int VPT, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const NormLaunch p) {
   __shared__ double red_d[kMaxWarps];
   __shared__ uint32_t red_u[kMaxWarps];
   pdl_wait();
@@ -192,20 +257,12 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch p) {
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    float f[8];
-    unpack8(raw[i], f);
     if (p.residual) {
-      float a[8];
-      unpack8(add[i], a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += a[j];
-      raw[i] = pack8(f);
+      raw[i] = add8(raw[i], add[i]);
       const int v = i * blockDim.x + threadIdx.x;
       if (p.r_out && v < nvec) reinterpret_cast<uint4*>(p.r_out + row * p.H)[v] = raw[i];
-      unpack8(raw[i], f);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += static_cast<double>(f[j] * f[j]);
+    sum = squares8(raw[i], sum);
   }
   const float rstd = rstd_of(block_sum(sum, red_d), p.inv_h, p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
@@ -213,20 +270,15 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch p) {
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * blockDim.x + threadIdx.x;
-    float f[8], w[8];
-    unpack8(raw[i], f);
-    unpack8(wv[i], w);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[j] = f[j] * rstd * w[j];
-      if (v < nvec) m = max(m, abs_bits(f[j]));   // outside the row 0 * rstd may be NaN
-    }
-    if (p.y && v < nvec) reinterpret_cast<uint4*>(p.y + row * p.H)[v] = pack8(f);
+    float2 y[4];
+    float big = 0.0f;
+    normed8(raw[i], wv[i], rstd, y, big);
+    const uint32_t m = v < nvec ? __float_as_uint(big) : 0u;      // outside the row 0 * rstd may be NaN
+    if (p.y && v < nvec) reinterpret_cast<uint4*>(p.y + row * p.H)[v] = pack8(y);
     if (p.q_format == E4B_Q8_MX) {
       const uint32_t byte = block_byte(m);
       if (v < nvec) {
-        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = mx_codes(f, byte);
+        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = mx_codes(y, byte);
         if ((v & 3) == 0) static_cast<uint8_t*>(p.q_scales)[row * (p.H >> 5) + (v >> 2)] = static_cast<uint8_t>(byte);
       }
     }
@@ -240,12 +292,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormLaunch p) {
     for (int i = 0; i < VPT; ++i) {
       const int v = i * blockDim.x + threadIdx.x;
       if (v >= nvec) continue;
-      float f[8], w[8];
-      unpack8(raw[i], f);
-      unpack8(wv[i], w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
-      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = row_codes(f, s, amax);
+      float2 y[4];
+      float big = 0.0f;
+      normed8(raw[i], wv[i], rstd, y, big);
+      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = row_codes(y, s, amax);
     }
   }
 }
@@ -273,22 +323,12 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormLaunch p) {
     for (int i = 0; i < VPT; ++i) add[i] = 32 * i + lane < nvec ? res[32 * i + lane] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      float f[8], a[8];
-      unpack8(raw[i], f);
-      unpack8(add[i], a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += a[j];
-      raw[i] = pack8(f);
+      raw[i] = add8(raw[i], add[i]);
       if (p.r_out && 32 * i + lane < nvec) reinterpret_cast<uint4*>(p.r_out + row * p.H)[32 * i + lane] = raw[i];
     }
   }
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    float f[8];
-    unpack8(raw[i], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += static_cast<double>(f[j] * f[j]);
-  }
+  for (int i = 0; i < VPT; ++i) sum = squares8(raw[i], sum);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
   const float rstd = rstd_of(sum, p.inv_h, p.eps);
@@ -299,21 +339,15 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormLaunch p) {
   for (int i = 0; i < VPT; ++i) {
     const int v = 32 * i + lane;
     const bool in = v < nvec;
-    float f[8], w[8];
-    unpack8(raw[i], f);
-    unpack8(in ? __ldg(weight + v) : make_uint4(0, 0, 0, 0), w);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[j] = f[j] * rstd * w[j];
-      m = max(m, abs_bits(f[j]));
-    }
-    if (!in) m = 0;                                // outside the row 0 * rstd may be NaN
-    if (p.y && in) reinterpret_cast<uint4*>(p.y + row * p.H)[v] = pack8(f);
+    float2 y[4];
+    float big = 0.0f;
+    normed8(raw[i], in ? __ldg(weight + v) : make_uint4(0, 0, 0, 0), rstd, y, big);
+    const uint32_t m = in ? __float_as_uint(big) : 0u;            // outside the row 0 * rstd may be NaN
+    if (p.y && in) reinterpret_cast<uint4*>(p.y + row * p.H)[v] = pack8(y);
     if (p.q_format == E4B_Q8_MX) {
       const uint32_t byte = block_byte(m);
       if (in) {
-        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = mx_codes(f, byte);
+        reinterpret_cast<uint2*>(p.q + row * p.H)[v] = mx_codes(y, byte);
         if ((v & 3) == 0) static_cast<uint8_t*>(p.q_scales)[row * (p.H >> 5) + (v >> 2)] = static_cast<uint8_t>(byte);
       }
     }
@@ -327,12 +361,10 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormLaunch p) {
     for (int i = 0; i < VPT; ++i) {
       const int v = 32 * i + lane;
       if (v >= nvec) continue;
-      float f[8], w[8];
-      unpack8(raw[i], f);
-      unpack8(__ldg(weight + v), w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
-      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = row_codes(f, s, amax);
+      float2 y[4];
+      float big = 0.0f;
+      normed8(raw[i], __ldg(weight + v), rstd, y, big);
+      reinterpret_cast<uint2*>(p.q + row * p.H)[v] = row_codes(y, s, amax);
     }
   }
 }
@@ -586,6 +618,12 @@ int threads_for(int H, int vpt) {
   return ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
 }
 
+// A block per row.  The block counts that go with the kernels keep their registers at what full residency allows.
+template <int VPT, int THREADS, int BLOCKS>
+cudaError_t launch_rows(const NormLaunch& p, cudaStream_t s) {
+  return launch_pdl(norm_kernel<VPT, THREADS, BLOCKS>, dim3(p.T), dim3(threads_for(p.H, VPT)), 0, s, p);
+}
+
 template <typename DY, int VPT, int STAGES>
 cudaError_t launch_backward_vec(const NormBackwardLaunch& p, int blocks, cudaStream_t s) {
   auto kern = norm_backward_kernel<DY, VPT, STAGES>;
@@ -636,13 +674,13 @@ cudaError_t launch_rmsnorm(const NormLaunch& p, cudaStream_t s) {
       if (p.H <= 512) return launch_pdl(norm_warp_kernel<2>, grid, block, 0, s, p);
       return launch_pdl(norm_warp_kernel<4>, grid, block, 0, s, p);
     }
-    if (p.H <= 2048) return launch_pdl(norm_kernel<2>, dim3(p.T), dim3(threads_for(p.H, 2)), 0, s, p);
-    if (p.H <= 2944) return launch_pdl(norm_kernel<3>, dim3(p.T), dim3(threads_for(p.H, 3)), 0, s, p);
-    return launch_pdl(norm_kernel<4>, dim3(p.T), dim3(threads_for(p.H, 4)), 0, s, p);
+    if (p.H <= 2048) return launch_rows<2, 128, 12>(p, s);
+    if (p.H <= 2944) return launch_rows<3, 128, 8>(p, s);
+    return launch_rows<4, 128, 8>(p, s);
   }
-  if (p.H <= 2048) return launch_pdl(norm_kernel<1>, dim3(p.T), dim3(threads_for(p.H, 1)), 0, s, p);
-  if (p.H <= 8192) return launch_pdl(norm_kernel<2>, dim3(p.T), dim3(threads_for(p.H, 2)), 0, s, p);
-  return launch_pdl(norm_kernel<4>, dim3(p.T), dim3(threads_for(p.H, 4)), 0, s, p);
+  if (p.H <= 2048) return launch_rows<1, 256, 8>(p, s);
+  if (p.H <= 8192) return launch_rows<2, 512, 3>(p, s);
+  return launch_rows<4, 1024, 1>(p, s);
 }
 
 // One row of partial weight gradients per block: one block per SM, fewer for few rows.
