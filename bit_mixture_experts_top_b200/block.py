@@ -270,6 +270,6 @@ class GradClipper:
             first = self.grads.tensors[0][0]
             norm = first.new_empty((), dtype=torch.float32)
             ws = first.new_empty(self.ws_bytes, dtype=torch.uint8)
-            e4b._check(e4b.lib().e4b_clip_grad_norm(self._table, len(self.grads), max_norm, norm.data_ptr(), ws.data_ptr(),
+            e4b._check(e4b.lib().e4b_clip_grad_norm(self._table, len(self.grads), float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                                     self.ws_bytes, e4b._stream(None)), "e4b_clip_grad_norm")
         return norm

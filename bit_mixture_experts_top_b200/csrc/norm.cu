@@ -8,7 +8,7 @@
 //   y    = fl32(fl32(r * rstd) * w)    -> bf16, or e4m3 with scales
 // What is normed is the rounded r: it is the stream that the next block and
 // the backward see.  The statistics are held in fp64 (the squares of bf16
-// values are exact in fp32, so only the sum rounds): rstd is then the same
+// values are exact there, so only the sum rounds): rstd is then the same
 // fp32 value for every summation order, and an 8-bit code next to a rounding
 // border does not depend on how the row was split over threads.
 //
@@ -99,14 +99,14 @@ __device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Sum of the eight squares (each exact in fp32), in fp64.
+// Adds the eight squares in fp64 (each exact there, whatever its size).
 __device__ __forceinline__ double squares8(const uint4& v, double sum) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = pair_of(w[i]), q = mul2(f, f);
-    sum += static_cast<double>(q.x);
-    sum += static_cast<double>(q.y);
+    const float2 f = pair_of(w[i]);
+    sum = fma(static_cast<double>(f.x), static_cast<double>(f.x), sum);
+    sum = fma(static_cast<double>(f.y), static_cast<double>(f.y), sum);
   }
   return sum;
 }
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormLaunch p) {
   for (int h = threadIdx.x; h < p.H; h += blockDim.x) {
     const float r = stream_value(h);
     if (p.residual && p.r_out) p.r_out[at + h] = static_cast<uint16_t>(__float_as_uint(r) >> 16);
-    sum += static_cast<double>(r * r);
+    sum = fma(static_cast<double>(r), static_cast<double>(r), sum);
   }
   const float rstd = rstd_of(block_sum(sum, red_d), p.inv_h, p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[blockIdx.x] = rstd;

@@ -125,6 +125,40 @@ def test_misaligned_rows(shift):
     assert np.array_equal(to_np_bits(y), bf16.f64_to_bf16_bits(wy.astype(np.float64)))
 
 
+@pytest.mark.parametrize("H", [64, 2048, 2056, 4096, 8200, 33])
+def test_subnormals_and_signed_zeros(H):
+    g = np.random.default_rng(H)
+    sub = lambda: (g.integers(0, 0x80, (4, H)) | (g.integers(0, 2, (4, H)) << 15)).astype(np.uint16)  # noqa: E731
+    x, res, w = sub(), sub(), _bits((H,), "sw")
+    res[1] = x[1] ^ 0x8000                                # sums that cancel
+    res[2], x[2] = 0x8000, 0x8000                         # -0 + -0
+    for eps in (0.0, 1e-30, 1e-6):
+        norm = block.RmsNorm(_dev(w), eps)
+        y, r, rstd = norm.forward_train(_dev(x), _dev(res))
+        wr, ws, wy = dense.rmsnorm(x, res, w, eps)
+        assert np.array_equal(to_np_bits(r), wr) and np.array_equal(rstd.cpu().numpy(), ws)
+        fine = np.isfinite(wy)                            # a row of zeros without eps is 0 * inf
+        assert np.array_equal(to_np_bits(y)[fine], bf16.f64_to_bf16_bits(wy.astype(np.float64))[fine])
+        assert np.isnan(bf16_to_f64(y)[~fine]).all()
+        q, s, _ = norm.forward_q8(_dev(x), _dev(res), scales="row")
+        wq, wsc = dense.quantize_rows(wy)
+        assert np.array_equal(q.view(torch.uint8).cpu().numpy(), wq)
+        assert np.array_equal(s.cpu().numpy(), wsc, equal_nan=True)
+
+
+@pytest.mark.parametrize("H", [64, 2056, 33])
+def test_values_whose_squares_leave_the_fp32_range(H):
+    x, _, w = _inputs(5, H, False)
+    x[0] = _bits((H,), "huge", 2.0 ** 100)
+    x[3] = _bits((H,), "small", 2.0 ** -100)
+    norm = block.RmsNorm(_dev(w), 0.0)
+    y, r, rstd = norm.forward_train(_dev(x))
+    _, ws, wy = dense.rmsnorm(x, None, w, 0.0)
+    fine = np.isfinite(wy)
+    assert fine[[0, 2, 3, 4]].all() and np.array_equal(rstd.cpu().numpy(), ws)
+    assert np.array_equal(to_np_bits(y)[fine], bf16.f64_to_bf16_bits(wy.astype(np.float64))[fine])
+
+
 def test_no_rows():
     norm = block.RmsNorm(_dev(_bits((64,), "w")))
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=device())
