@@ -517,16 +517,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 // launch does not write it (b_early): the first stages then hide its tail.
 struct SplitCfg {
   static constexpr int BN = 128, SK = 128;
-  static constexpr int A_BYTES = BM * SK * 2, B_BYTES = BN * SK * 2, ATOM = BM * BK * 2;   // an atom: 64 of K
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 3;
+  static constexpr int ATOM = BM * BK * 2;                    // 128 rows of 64 K
+  static constexpr int RING_BYTES = 196608;                   // three stages of two atoms of A and two of B, or four
+  static constexpr int MAX_STAGES = 4;                        // with half atoms of A
   static constexpr int PITCH = BN + 4;                        // floats per row of the partial tile (conflict-free)
   static constexpr int OFF_SUMS = BM * PITCH * 4;             // dact: column sums per warp, behind the partial tile
-  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 1) * 8;
+  static constexpr int OFF_BAR = RING_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * MAX_STAGES + 1) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int EPI = 8, THREADS = 32 * (WARP_EPI0 + EPI);
-  static_assert(OFF_SUMS + EPI * 2 * BN * 4 <= STAGES * STAGE_BYTES, "both reuse the stages");
+  static_assert(OFF_SUMS + EPI * 2 * BN * 4 <= RING_BYTES, "both reuse the stages");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -558,14 +558,19 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* empty = full + C::MAX_STAGES;
+  uint64_t* acc_full = empty + C::MAX_STAGES;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int32_t* s_abort = reinterpret_cast<int32_t*>(smem + C::OFF_MISC + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
+  // Up to 64 rows A is loaded in half atoms: what the MMA reads behind them (the next atom) only reaches rows of D
+  // that nobody reads, and the ring holds four stages.
+  const bool half_a = !A_MN && p.M <= BM / 2;
+  const int a_atom = half_a ? C::ATOM / 2 : C::ATOM, stages = half_a ? 4 : 3;
+  const int stage_bytes = 2 * (a_atom + C::ATOM);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -598,8 +603,8 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     uint32_t phase = 0, armed = 0, par = 0;
     bool ok = true;
     auto load_a = [&](int ks, int stage) {
-      uint8_t* a = smem + stage * C::STAGE_BYTES;
-      for (int i = 0; i < atoms_of(ks); ++i, a += C::ATOM) {
+      uint8_t* a = smem + stage * stage_bytes;
+      for (int i = 0; i < atoms_of(ks); ++i, a += a_atom) {
         const int k0 = ks * C::SK + i * BK;
         if constexpr (A_MN) {
           tma_load_2d(a, &tm_a, &full[stage], m0, k0);
@@ -610,8 +615,8 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
       }
     };
     auto load_b = [&](int ks, int stage) {
-      uint8_t* b = smem + stage * C::STAGE_BYTES + C::A_BYTES;
-      mbar_arrive_expect_tx(&full[stage], atoms_of(ks) * 2 * C::ATOM);
+      uint8_t* b = smem + stage * stage_bytes + 2 * a_atom;
+      mbar_arrive_expect_tx(&full[stage], atoms_of(ks) * (a_atom + C::ATOM));
       for (int i = 0; i < atoms_of(ks); ++i, b += C::ATOM) {
         const int k0 = ks * C::SK + i * BK;
         if constexpr (EPI == kEpiGateUp) {
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
         }
       }
     };
-    const int early = p.b_early ? min(C::STAGES, last - first) : 0;
+    const int early = p.b_early ? min(stages, last - first) : 0;
     if (elect_one())
       for (int i = 0; i < early; ++i) load_b(first + i, i);
     __syncwarp();
@@ -640,17 +645,17 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
       __syncwarp();
       armed |= 1u << stage;
       par = (par & ~(1u << stage)) | (phase << stage);
-      if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+      if (++stage == stages) { stage = 0; phase ^= 1u; }
     }
     if (!ok && lane == 0) {
-      for (int s = 0; s < C::STAGES; ++s)
+      for (int s = 0; s < stages; ++s)
         if (armed & (1u << s)) mbar_drain(&full[s], (par >> s) & 1u, kDrainNs);
     }
   } else if (warp == WARP_MMA) {
     constexpr uint32_t idesc = idesc_bf16_f32(BM, C::BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
     const uint32_t base = smem_u32(smem);
     const uint64_t da0 = A_MN ? smem_desc_mn_sw128(base) : smem_desc_sw128(base);
-    const uint64_t db0 = B_MN ? smem_desc_mn_sw128(base + C::A_BYTES) : smem_desc_sw128(base + C::A_BYTES);
+    const uint64_t db0 = B_MN ? smem_desc_mn_sw128(base + 2 * a_atom) : smem_desc_sw128(base + 2 * a_atom);
     constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
     int stage = 0;
     uint32_t phase = 0;
@@ -660,14 +665,14 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     for (int ks = first; ks < last; ++ks) {
       if (!mbar_wait_warp(&full[stage], phase, wctx, 1502)) { ok = false; break; }
       const int atoms = atoms_of(ks);
-      const uint64_t da = da0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
-      const uint64_t db = db0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+      const uint64_t da = da0 + static_cast<uint32_t>(stage * (stage_bytes >> 4));
+      const uint64_t db = db0 + static_cast<uint32_t>(stage * (stage_bytes >> 4));
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < C::SK / 16; ++kk) {
           if (kk >= 4 * atoms) break;
-          const uint32_t off = (kk >> 2) * (C::ATOM >> 4);
-          umma_bf16_ss(tmem_base, da + off + (kk & 3) * a_step, db + off + (kk & 3) * b_step, idesc,
+          umma_bf16_ss(tmem_base, da + static_cast<uint32_t>((kk >> 2) * (a_atom >> 4) + (kk & 3) * a_step),
+                       db + (kk >> 2) * (C::ATOM >> 4) + (kk & 3) * b_step, idesc,
                        (ks > first || kk > 0) ? 1u : 0u);
         }
         umma_commit(&empty[stage]);
@@ -675,10 +680,10 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
       }
       __syncwarp();
       issued = true;
-      if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+      if (++stage == stages) { stage = 0; phase ^= 1u; }
     }
     if (!ok && issued && lane == 0)
-      mbar_drain(&empty[stage == 0 ? C::STAGES - 1 : stage - 1], stage == 0 ? phase ^ 1u : phase, kDrainNs);
+      mbar_drain(&empty[stage == 0 ? stages - 1 : stage - 1], stage == 0 ? phase ^ 1u : phase, kDrainNs);
   } else if (warp >= WARP_EPI0) {
     // this CTA's partial tile into its shared memory (every stage has been consumed by then)
     const int q = warp & 3, half = (warp - WARP_EPI0) >> 2;
@@ -1013,13 +1018,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Tensor maps of both operands.  K-contiguous: [rows, K], boxes of 64 K x tile rows; M/N-contiguous:
 // [K, rows], boxes of 64 rows x 64 K.
 template <bool A_MN, bool B_MN, int EPI>
-bool encode_operands(const DenseGemmLaunch& g, int b_box, CUtensorMap* ta, CUtensorMap* tb) {
+bool encode_operands(const DenseGemmLaunch& g, int b_box, CUtensorMap* ta, CUtensorMap* tb, int a_box = BM) {
   const uint64_t b_rows = EPI == kEpiGateUp ? 2 * static_cast<uint64_t>(g.N) : g.N;
   auto enc = [](CUtensorMap* m, const uint16_t* p, uint64_t rows, uint64_t K, bool mn, int box) {
     return mn ? encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rows, K, rows * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)
               : encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, K, rows, K * 2, BK, box, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  return enc(ta, g.a, g.M, g.K, A_MN, BM) && enc(tb, g.b, b_rows, g.K, B_MN, b_box);
+  return enc(ta, g.a, g.M, g.K, A_MN, a_box) && enc(tb, g.b, b_rows, g.K, B_MN, b_box);
 }
 
 Params make_params(const DenseGemmLaunch& g, int tile_rows, int width, int tile_cols, int split = 1) {
@@ -1099,7 +1104,7 @@ template <bool A_MN, bool B_MN, int EPI>
 e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
   constexpr int NT = EPI == kEpiGateUp ? SplitCfg::BN / 2 : SplitCfg::BN;
   CUtensorMap ta, tb;
-  if (!encode_operands<A_MN, B_MN, EPI>(g, NT, &ta, &tb)) return E4B_ERR_CUDA;
+  if (!encode_operands<A_MN, B_MN, EPI>(g, NT, &ta, &tb, g.M <= BM / 2 ? BM / 2 : BM)) return E4B_ERR_CUDA;
   const Params p = make_params(g, BM, SplitCfg::BN, NT, S);
   if (g.colsum_rows) *g.colsum_rows = p.m_tiles * S;
   const dim3 grid(static_cast<unsigned>(p.m_tiles * p.n_tiles * S));
