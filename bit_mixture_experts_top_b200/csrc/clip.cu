@@ -11,10 +11,16 @@
 // needs no clearing.  Squares are formed and summed in fp64, so values whose
 // square leaves the fp32 range still count (a gradient of 1e25, or of 1e-30).
 //
-// Both passes are bound by HBM.  Work is dealt in chunks of 16 KB (32 KB in long
-// lists): four (eight) 16-byte loads per thread, eight blocks per SM.  The
-// second pass walks the chunks from the last to the first, so that what the
-// first pass read last is still in L2.
+// (A list of more than kMaxTable tensors takes several launches of each kind and
+// one that sums the partials once for all the scaling blocks.)
+//
+// Both passes are bound by HBM; the second starts where the first ended, so that
+// what was read last is still in L2.  In long lists a chunk is 32 KB, eight
+// 16-byte loads per thread, and the scaling pass gives each a block of its own:
+// 96 tensors, 705 MB, in 317 us (with eight blocks per SM that walk their chunks
+// 343: the blocks drift apart, and what is in L2 is gone before its turn).  In
+// short lists a chunk is 16 KB for the norm and 8 KB for scaling, whose blocks
+// need fewer registers with it: 401 ragged tensors, 92 MB, in 47 us (51 with 16 KB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,7 +37,7 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
 constexpr int kSmall = 64, kMedium = 256, kMaxTable = 960;   // 2, 8 and 30 KB of kernel arguments
 constexpr int kBlocksPerSm = 8;
-__host__ __device__ constexpr int words_per_thread(bool is_long) { return is_long ? 8 : 4; }   // 16-byte words per chunk
+constexpr int kNormWords = 4, kScaleWords = 2, kLongWords = 8;   // 16-byte words per thread and chunk
 constexpr size_t kLongBytes = size_t(160) << 20;   // a launch's tensors from which on chunks are long and strided
 
 // One tensor of the table.  Its 16-byte words start at the boundary at or
@@ -48,33 +54,23 @@ struct ClipEntry {
 
 template <int N>
 struct ClipTable {
-  int32_t tensors, chunks, strided;
+  int32_t tensors, chunks;
   ClipEntry e[N];
 };
 
 template <int TYPE>
 __host__ __device__ constexpr int size_of() { return TYPE == E4B_F32 ? 4 : 2; }
 
-// Which tensor a chunk belongs to, by bisection in shared memory (the table itself lies in the argument bank, whose
-// cache misses cost more than the search).
+// The last tensor whose first chunk is at or before this one: by bisection in the
+// argument bank, where a block's threads agree on every step.  (A copy of the
+// table's chunks in shared memory cost each block more than its searches: 900
+// tensors of 1 MB took 460 us against 423.)
 template <int N>
-struct ChunkIndex {
-  int32_t first[N];
-
-  __device__ __forceinline__ void fill(const ClipTable<N>& t) {   // (a warp reads one entry at a time: lanes that
-    for (int i = threadIdx.x >> 5; i < t.tensors; i += kThreads / 32)   // differ would be served one by one)
-      if ((threadIdx.x & 31) == 0) first[i] = t.e[i].chunk0;
-    __syncthreads();
-  }
-};
-
-// The last tensor whose first chunk, first_of(i), is at or before this one.
-template <typename First>
-__device__ __forceinline__ int tensor_of(int tensors, int chunk, const First& first_of) {
-  int lo = 0, hi = tensors;
+__device__ __forceinline__ int tensor_of(const ClipTable<N>& t, int chunk) {
+  int lo = 0, hi = t.tensors;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (first_of(mid) <= chunk) lo = mid; else hi = mid;
+    if (t.e[mid].chunk0 <= chunk) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -83,21 +79,21 @@ __device__ __forceinline__ int tensor_of(int tensors, int chunk, const First& fi
 // the whole list, so that the blocks move through memory together, the tensor
 // found anew for each chunk.  Short lists, mostly of small tensors: one
 // contiguous run, whose next chunk lies in the same tensor or the one beside it.
-// REVERSED: the same chunks from the last to the first.
-template <int N, bool LONG, bool REVERSED, typename Index, typename Body>
-__device__ __forceinline__ void walk_chunks(const ClipTable<N>& t, const Index& index, const Body& body) {
-  const int b = blockIdx.x, n = gridDim.x;
+// REVERSED: from the last block's last chunk to the first's first.
+template <int N, bool LONG, bool REVERSED, typename Body>
+__device__ __forceinline__ void walk_chunks(const ClipTable<N>& t, const Body& body) {
+  const int n = gridDim.x, b = REVERSED ? n - 1 - static_cast<int>(blockIdx.x) : blockIdx.x;
   if constexpr (LONG) {
     const int count = b < t.chunks ? (t.chunks - 1 - b) / n + 1 : 0;
     for (int i = 0; i < count; ++i) {
       const int c = b + (REVERSED ? count - 1 - i : i) * n;
-      body(t.e[tensor_of(t.tensors, c, [&](int j) { return index.first[j]; })], c);
+      body(t.e[tensor_of(t, c)], c);
     }
   } else {
     const int c0 = static_cast<int>(static_cast<int64_t>(t.chunks) * b / n);
     const int c1 = static_cast<int>(static_cast<int64_t>(t.chunks) * (b + 1) / n);
     if (c0 == c1) return;
-    int ti = tensor_of(t.tensors, REVERSED ? c1 - 1 : c0, [&](int j) { return t.e[j].chunk0; });
+    int ti = tensor_of(t, REVERSED ? c1 - 1 : c0);
     for (int i = 0; i < c1 - c0; ++i) {
       const int c = REVERSED ? c1 - 1 - i : c0 + i;
       if constexpr (REVERSED) {
@@ -167,33 +163,33 @@ __device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
 }
 
 // Calls word(i) for this thread's words of the chunk that lie wholly inside the
-// tensor and one(k) for the single elements of its first and last word.  A
-// chunk in the tensor's middle is only whole words and takes no tests.
+// tensor and one(k) for the single elements of its first and last word, each
+// by another thread.  A chunk in the tensor's middle is only whole words and
+// takes no tests.
 template <int TYPE, int V, typename Word, typename One>
 __device__ __forceinline__ void for_chunk(const ClipEntry& e, int64_t w0, const Word& word, const One& one) {
   constexpr int PER = 16 / size_of<TYPE>();
   const int64_t last = e.n + e.skip;                      // elements counted from the first word's start
   const int64_t c0 = w0 - threadIdx.x;
+  const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>()) + w0;
   if (c0 * PER >= e.skip && (c0 + V * kThreads) * PER <= last) {
     uint4 v[V];
-    const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>()) + w0;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = in[i * kThreads];
 #pragma unroll
     for (int i = 0; i < V; ++i) word(w0 + i * kThreads, v[i]);
     return;
   }
-  const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(e.in) - e.skip * size_of<TYPE>());
-  for (int i = 0; i < V; ++i) {
-    const int64_t w = w0 + i * kThreads, at = w * PER;
-    if (at >= last) break;
-    if (at >= e.skip && at + PER <= last) {
-      word(w, in[w]);
-    } else {
-      for (int j = 0; j < PER; ++j)
-        if (at + j >= e.skip && at + j < last) one(at + j - e.skip);
-    }
+  const int64_t begin = (e.skip + PER - 1) / PER, end = last / PER;   // the whole words
+  const int64_t head = begin * PER - e.skip;              // elements before them
+  if (c0 == 0 && threadIdx.x < head && threadIdx.x < e.n) one(threadIdx.x);
+  if (end >= begin && c0 <= end && end < c0 + V * kThreads) {
+    const int64_t k = end * PER - e.skip + static_cast<int>(kThreads - 1 - threadIdx.x);
+    if (k < e.n) one(k);
   }
+  const int64_t stop = end < c0 + V * kThreads ? end : c0 + V * kThreads;
+#pragma unroll 2
+  for (int64_t w = w0 < begin ? w0 + kThreads : w0; w < stop; w += kThreads) word(w, in[w - w0]);
 }
 
 template <int TYPE, int V>
@@ -249,13 +245,11 @@ template <int N, bool LONG>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ ClipTable<N> t,
                                                              double* __restrict__ partial) {
   __shared__ double red[kThreads / 32];
-  __shared__ ChunkIndex<LONG ? N : 1> index;
-  if constexpr (LONG) index.fill(t);
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int V = words_per_thread(LONG);
+  constexpr int V = LONG ? kLongWords : kNormWords;
   double sum = 0.0;
-  walk_chunks<N, LONG, false>(t, index, [&](const ClipEntry& e, int c) {
+  walk_chunks<N, LONG, false>(t, [&](const ClipEntry& e, int c) {
     const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * (V * kThreads) + threadIdx.x;
     if (e.type == E4B_F32) sum += chunk_squares<E4B_F32, V>(e, w0);
     else if (e.type == E4B_BF16) sum += chunk_squares<E4B_BF16, V>(e, w0);
@@ -271,18 +265,16 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
                                                               const double* __restrict__ partial, int partials,
                                                               double max_norm, float* __restrict__ total_norm) {
   __shared__ double red[kThreads / 32];
-  __shared__ ChunkIndex<LONG ? N : 1> index;
-  if constexpr (LONG) index.fill(t);
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int V = words_per_thread(LONG);
+  constexpr int V = LONG ? kLongWords : kScaleWords;
   double sum = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
   const double norm = sqrt(block_sum(sum, red));
   if (total_norm && blockIdx.x == 0 && threadIdx.x == 0) *total_norm = static_cast<float>(norm);
   const double ratio = max_norm / (norm + 1e-6);
   const float coef = isinf(max_norm) || ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);   // a NaN norm gives NaN
-  walk_chunks<N, LONG, true>(t, index, [&](const ClipEntry& e, int c) {
+  walk_chunks<N, LONG, true>(t, [&](const ClipEntry& e, int c) {
     if (e.in == e.out && coef == 1.0f) return;            // in place and unclipped: already there
     const int64_t w0 = static_cast<int64_t>(c - e.chunk0) * (V * kThreads) + threadIdx.x;
     if (e.type == E4B_F32) chunk_scale<E4B_F32, V>(e, w0, coef);
@@ -291,9 +283,20 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
   });
 }
 
+// One sum of many partials, for the blocks of several scale launches.
+__global__ void __launch_bounds__(kThreads) grad_sum_kernel(double* __restrict__ partial, int partials) {
+  __shared__ double red[kThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
+  sum = block_sum(sum, red);
+  if (threadIdx.x == 0) partial[0] = sum;
+}
+
 template <int N>
-void fill_table(ClipTable<N>& t, const e4b_grad* g, int count, bool is_long) {
-  const int64_t chunk_bytes = 16 * kThreads * words_per_thread(is_long);
+void fill_table(ClipTable<N>& t, const e4b_grad* g, int count, int words) {
+  const int64_t chunk_bytes = 16 * kThreads * words;
   t.tensors = count;
   int64_t chunk = 0;
   for (int i = 0; i < count; ++i) {
@@ -312,9 +315,17 @@ void fill_table(ClipTable<N>& t, const e4b_grad* g, int count, bool is_long) {
   t.chunks = static_cast<int32_t>(chunk);
 }
 
-int blocks_for(int chunks) {
-  const int cap = device_sm_count() * kBlocksPerSm;
-  return chunks < cap ? (chunks > 0 ? chunks : 1) : cap;
+int at_least_one(int64_t chunks, int64_t cap) { return static_cast<int>(chunks < cap ? (chunks > 0 ? chunks : 1) : cap); }
+
+// One partial sum per block, so a bounded number of them.
+int norm_blocks(int chunks) { return at_least_one(chunks, int64_t(device_sm_count()) * kBlocksPerSm); }
+
+// In short lists a block sums the partials once for several chunks: 16 blocks per
+// SM where each still has four (47 us for the 401 tensors, 49 with 8), else 8
+// (9.5 us for 15 MB, 9.8 with 16).
+int scale_blocks(int chunks, bool is_long) {
+  const int64_t sms = device_sm_count();
+  return is_long ? at_least_one(chunks, chunks) : at_least_one(chunks, chunks >= 64 * sms ? 16 * sms : 8 * sms);
 }
 
 // Both kernels for `count` tensors; partial and the count of what is in it move on with the norm pass.
@@ -327,15 +338,15 @@ struct ClipRun {
   template <int N, bool LONG>
   cudaError_t norm(double* partial, int* blocks) const {
     ClipTable<N> t;
-    fill_table(t, g, count, LONG);
-    *blocks = blocks_for(t.chunks);
+    fill_table(t, g, count, LONG ? kLongWords : kNormWords);
+    *blocks = norm_blocks(t.chunks);
     return launch_pdl(grad_norm_kernel<N, LONG>, dim3(*blocks), dim3(kThreads), 0, s, t, partial);
   }
   template <int N, bool LONG>
   cudaError_t scale(const double* partial, int partials, double max_norm, float* total_norm) const {
     ClipTable<N> t;
-    fill_table(t, g, count, LONG);
-    return launch_pdl(grad_scale_kernel<N, LONG>, dim3(blocks_for(t.chunks)), dim3(kThreads), 0, s, t, partial,
+    fill_table(t, g, count, LONG ? kLongWords : kScaleWords);
+    return launch_pdl(grad_scale_kernel<N, LONG>, dim3(scale_blocks(t.chunks, LONG)), dim3(kThreads), 0, s, t, partial,
                       partials, max_norm, total_norm);
   }
   cudaError_t norm(double* partial, int* blocks) const {
@@ -374,6 +385,11 @@ cudaError_t launch_clip_grads(const e4b_grad* g, int32_t tensors, double max_nor
     const cudaError_t e = run_at(i).norm(partial + partials, &blocks);
     if (e != cudaSuccess) return e;
     partials += blocks;
+  }
+  if (tensors > kMaxTable) {
+    const cudaError_t e = launch_pdl(grad_sum_kernel, dim3(1), dim3(kThreads), 0, s, partial, partials);
+    if (e != cudaSuccess) return e;
+    partials = 1;
   }
   for (int32_t k = 0; k < tensors; ++k) in_place = in_place && (g[k].n == 0 || g[k].grad == g[k].out);
   // only the norm is wanted and nothing moves: one block writes it
