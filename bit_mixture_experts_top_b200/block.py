@@ -71,10 +71,10 @@ class RmsNorm:
             if q_format == e4b.E4B_Q8_NONE:
                 y = torch.empty_like(x)
             else:
-                q = x.new_empty((T, H), dtype=torch.float8_e4m3fn)
-                scales = x.new_empty((T,), dtype=torch.float32) if q_format == e4b.E4B_Q8_ROW else \
+                q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+                scales = x.new_empty(T, dtype=torch.float32) if q_format == e4b.E4B_Q8_ROW else \
                     x.new_empty((T, H // 32), dtype=torch.uint8)
-            rstd = x.new_empty((T,), dtype=torch.float32) if want_rstd else None
+            rstd = x.new_empty(T, dtype=torch.float32) if want_rstd else None
             # (the tensors are checked: straight to the library, whose call costs a few microseconds in all)
             e4b._check(e4b.lib().e4b_rmsnorm(
                 x.data_ptr(), _ptr(residual), self.weight.data_ptr(), T, H, self.eps, q_format,

@@ -1116,12 +1116,19 @@ e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
 
 // Which kernel: estimated time in units of one 64-K step of a 256 x 256 pair
 // tile (0.28 us on a B200).  A narrower pair tile costs nearly its share, so a
-// width that fills the last wave of pairs may win over 256.  A step of a
-// 128 x 128 tile of one CTA costs 0.8 (issue-bound, whatever its width), a 128-K
-// step of the split kernel 1.7 (it waits for its loads) and its exchange about 6.
+// width that fills the last wave of pairs may win over 256.  A step of a tile of
+// one CTA, 128 rows high, costs 0.8 up to 128 columns (issue-bound) and grows to
+// 1.4 at 256 (its loads): tiles of 160 to 256 columns stream a large B past few
+// rows (gate and up of 4096 x 12288, 33 tokens: 192 columns 59.2 us with the
+// down product, 128 columns, whose second wave is a third full, 68.6).  A 128-K
+// step of the split kernel costs 1.7 (it waits for its loads), its exchange 2
+// and 1 for each CTA of a cluster.  Behind another launch of the library it
+// overlaps with that one's end only while some GPCs have room for a cluster
+// (23 clusters of 5 took 1.8 us more than 23 of 4).
+enum Kind { kPair, kSingle, kSplit };
 struct Choice {
-  int width;        // of pair tiles; 0: 128 x 128 tiles of one CTA
-  int split;        // > 1: the split kernel with clusters of this size
+  Kind kind;
+  int value;        // columns per tile, or the cluster size of the split kernel
   double time;
 };
 
@@ -1134,16 +1141,21 @@ Choice choose(const DenseGemmLaunch& g) {
   };
   auto waves = [](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
   const int64_t k64 = (g.K + BK - 1) / BK, k128 = (g.K + 127) / 128, t128 = tiles(128, 128);
-  Choice c{256, 1, waves(tiles(256, 256), sms / 2) * k64 + 4.0};
+  Choice c{kPair, 256, waves(tiles(256, 256), sms / 2) * k64 + 4.0};
   for (int w = 224; w >= 160; w -= 32) {
     const double t = waves(tiles(256, w), sms / 2) * k64 * (0.1 + 0.9 * w / 256.0) + 4.0;
-    if (t < 0.97 * c.time) c = Choice{w, 1, t};
+    if (t < 0.97 * c.time) c = Choice{kPair, w, t};
   }
-  const double single = waves(t128, sms) * k64 * 0.8;
-  if (single <= c.time) c = Choice{0, 1, single};
+  for (int w = 128; w <= 256; w += 32) {
+    const double t = waves(tiles(128, w), sms) * k64 * (0.8 + 0.6 * (w - 128) / 128.0);
+    if (w == 128 ? t <= c.time : t < 0.97 * c.time) c = Choice{kSingle, w, t};
+  }
   for (int n = 2; n <= 8 && n <= k128 && t128 * n <= sms; ++n) {
-    const double t = static_cast<double>((k128 + n - 1) / n) * 1.7 + 6.0;
-    if (t < c.time && t128 <= split_slots<A_MN, B_MN, EPI>(n)) c = Choice{0, n, t};
+    double t = static_cast<double>((k128 + n - 1) / n) * 1.7 + 2.0 + n;
+    if (t >= c.time) continue;
+    const int slots = split_slots<A_MN, B_MN, EPI>(n);
+    if (g.b_early && t128 > 0.85 * slots) t += 3.0;
+    if (t < c.time && t128 <= slots) c = Choice{kSplit, n, t};
   }
   return c;
 }
@@ -1151,10 +1163,11 @@ Choice choose(const DenseGemmLaunch& g) {
 template <bool A_MN, bool B_MN, int EPI>
 e4b_status launch_width(const DenseGemmLaunch& g, cudaStream_t s) {
   const Choice c = choose<A_MN, B_MN, EPI>(g);
-  if (c.split > 1) return launch_split<A_MN, B_MN, EPI>(g, c.split, s);
+  if (c.kind == kSplit) return launch_split<A_MN, B_MN, EPI>(g, c.value, s);
   if (g.colsum_rows) *g.colsum_rows = (g.M + 31) / 32;
-  if (c.width) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, c.width, s);
-  return launch_typed<128, 1, A_MN, B_MN, EPI>(g, 128, s);
+  if (c.kind == kPair) return launch_typed<256, 2, A_MN, B_MN, EPI>(g, c.value, s);
+  return c.value == 128 ? launch_typed<128, 1, A_MN, B_MN, EPI>(g, 128, s)
+                        : launch_typed<256, 1, A_MN, B_MN, EPI>(g, c.value, s);
 }
 
 }  // namespace

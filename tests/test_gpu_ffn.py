@@ -129,6 +129,18 @@ def test_training(T, H, I):
         assert only[1:] == (None, None, None, None)
 
 
+# one row of tiles of one CTA, 160, 192, 224 and 256 columns wide, for each of the three epilogues; two rows of them
+@pytest.mark.parametrize("T,H,I", [(40, 72, 11400), (40, 72, 12288), (121, 72, 16000), (40, 72, 18904), (17, 72, 23000),
+                                   (40, 72, 26008), (64, 72, 30000), (40, 72, 36000), (40, 23000, 72), (128, 26008, 72),
+                                   (40, 30000, 72), (97, 36000, 72), (200, 72, 6000), (129, 11400, 72)])
+def test_wide_tiles(T, H, I):
+    c = Case(T, H, I, glu=GLU, bias=True, add=True)
+    out, saved = c.ffn.forward_train(c.d["x"], c.d["add"])
+    c.check_out(out)
+    c.check_grads(c.ffn.backward(saved, c.d["dout"]))
+    c.check_out(c.ffn.forward(c.d["x"], c.d["add"]))
+
+
 def test_each_gradient_alone():
     c = Case(40, 136, 72, bias=True)
     _, saved = c.ffn.forward_train(c.d["x"])
