@@ -1123,8 +1123,8 @@ e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
 // down product, 128 columns, whose second wave is a third full, 68.6).  A 128-K
 // step of the split kernel costs 1.7 (it waits for its loads), its exchange 2
 // and 1 for each CTA of a cluster.  Behind another launch of the library it
-// overlaps with that one's end only while some GPCs have room for a cluster
-// (23 clusters of 5 took 1.8 us more than 23 of 4).
+// overlaps with that one's end only where clusters find room among its CTAs:
+// large ones that fill the device do not (23 of 5 took 1.8 us more than 23 of 4).
 enum Kind { kPair, kSingle, kSplit };
 struct Choice {
   Kind kind;
@@ -1154,7 +1154,7 @@ Choice choose(const DenseGemmLaunch& g) {
     double t = static_cast<double>((k128 + n - 1) / n) * 1.7 + 2.0 + n;
     if (t >= c.time) continue;
     const int slots = split_slots<A_MN, B_MN, EPI>(n);
-    if (g.b_early && t128 > 0.85 * slots) t += 3.0;
+    if (g.b_early && n > 4 && t128 > 0.85 * slots) t += 3.0;
     if (t < c.time && t128 <= slots) c = Choice{kSplit, n, t};
   }
   return c;
