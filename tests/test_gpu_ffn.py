@@ -141,6 +141,22 @@ def test_wide_tiles(T, H, I):
     c.check_out(c.ffn.forward(c.d["x"], c.d["add"]))
 
 
+# the products after dG in one launch on CTA pairs: ragged rows and columns, whole tiles, and two of the three
+@pytest.mark.parametrize("T,H,I", [(509, 2048, 768), (512, 2560, 256), (513, 2600, 264), (1300, 1800, 648),
+                                   (301, 2888, 2872), (2056, 1032, 1288)])
+def test_grouped_gradients(T, H, I):
+    c = Case(T, H, I, bias=True)
+    out, saved = c.ffn.forward_train(c.d["x"])
+    c.check_out(out)
+    full = c.ffn.backward(saved, c.d["dout"])
+    c.check_grads(full)
+    for keep in ("110", "101", "011"):
+        outs = [torch.full_like(t, 3.0) if k < 3 and keep[k] == "1" else None for k, t in enumerate(full)]
+        e4b.e4b_ffn_backward(c.ffn.desc, T, c.d["x"], c.d["dout"], c.d["gu"], c.d["dn"], *outs, saved.ws)
+        c.check_grads(outs)
+    assert e4b.e4b_device_status(saved.ws) == e4b.E4B_OK
+
+
 def test_each_gradient_alone():
     c = Case(40, 136, 72, bias=True)
     _, saved = c.ffn.forward_train(c.d["x"])
