@@ -834,12 +834,9 @@ e4b_status e4b_ffn_backward(const e4b_ffn_desc* d, int32_t T, const uint16_t* x,
     g.b = at<uint16_t>(ws, L.h);
     g.out = dw_dn;
   }
-  if (n > 0) st = launch_dense_group(rest, n, s);
-  if (st != E4B_OK) return st;
-  return launch_column_sums(at<float>(ws, L.gu_sums), sum_rows, 2 * d->I, dgu_bias, dout, T, d->H,
-                            at<float>(ws, L.dn_sums), ddn_bias, s) == cudaSuccess
-             ? E4B_OK
-             : E4B_ERR_CUDA;
+  const ColumnSums sums{at<float>(ws, L.gu_sums), sum_rows, 2 * d->I, dgu_bias, dout, T, d->H,
+                        at<float>(ws, L.dn_sums), ddn_bias};
+  return launch_dense_group(rest, n, sums, s);
 }
 
 static const int32_t kMaxGradTensors = 65536;

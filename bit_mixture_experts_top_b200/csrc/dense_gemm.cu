@@ -824,7 +824,9 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
 // steps and a fixed part) so that every CTA or pair gets an equal share of the
 // whole.  Pairs with tiles of 256 x 256 read each operand half as often as CTAs
 // with 128 x 128, which L2 bounds; small tiles deal better where there are few.  A is K- or row-contiguous per
-// product, B row-contiguous in all; the epilogue is the plain bf16 store.
+// product, B row-contiguous in all; the epilogue is the plain bf16 store.  Two
+// warps that have no other work form the bias gradients' column sums meanwhile
+// (5 us as a launch of their own).
 // Backward of 509 tokens at 2048 x 768: 31 us with pairs, 35 with small tiles, 38
 // one by one; at 2880 x 2880 71, 87 and 93.
 constexpr int kMultiMax = 3;
@@ -840,6 +842,7 @@ struct MultiParams {
   int32_t* status;
   uint64_t wait_limit_ns;
   MultiProblem p[kMultiMax];
+  ColumnSums sums;
 };
 
 struct alignas(64) MultiMaps {
@@ -866,6 +869,39 @@ __device__ __forceinline__ void walk_tiles(const MultiParams& mp, int share, int
     for (int t = first(lo); t < t1; ++t)
       if (!body(i, t)) return;
     at += mp.p[i].tiles * c;
+  }
+}
+
+// Column sums, a warp per strip of eight columns: a lane takes every 32nd row, then the lanes meet.
+__device__ __forceinline__ void sum_strips(const ColumnSums& c, int first, int step, int lane) {
+  const int strips_b = c.out_b ? c.Nb / 8 : 0, strips = strips_b + (c.out_a ? c.Na / 8 : 0);
+  for (int i = first; i < strips; i += step) {
+    float v[8] = {};
+    const bool is_b = i < strips_b;
+    const int at = 8 * (is_b ? i : i - strips_b);
+    if (is_b) {
+#pragma unroll 8
+      for (int r = lane; r < c.rows_b; r += 32) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(c.b + static_cast<int64_t>(r) * c.Nb + at));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] += __uint_as_float(u[j] << 16);
+          v[2 * j + 1] += __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int r = lane; r < c.rows_a; r += 32) {
+        float f[8];
+        load8f(c.a + static_cast<int64_t>(r) * c.Na + at, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+      }
+    }
+    int col;
+    const float sum = warp_column_sum8(v, lane, col);
+    if ((lane & 3) == 0) (is_b ? c.out_b : c.out_a)[at + col] = sum;
   }
 }
 
@@ -1000,6 +1036,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       return ok;
     });
     if (!ok && issued && lane == 0) mbar_drain(last_bar, last_par, kDrainNs);   // MMAs in flight finish first
+  } else if (warp > WARP_MMA && warp < WARP_EPI0) {
+    constexpr int kWarps = WARP_EPI0 - WARP_MMA - 1;
+    sum_strips(mp.sums, blockIdx.x * kWarps + warp - WARP_MMA - 1, gridDim.x * kWarps, lane);
   } else if (warp >= WARP_EPI0) {
     const int q4 = warp & 3, part = (warp - WARP_EPI0) >> 2;
     int it = 0;
@@ -1288,12 +1327,14 @@ e4b_status launch_multi(const DenseGemmLaunch* g, const MultiParams& mp, cudaStr
 // Plain linear products (no bias, no addition, B row-contiguous) that depend on earlier launches only: in one launch,
 // on CTAs or pairs, or one by one (which costs about 8 units for each launch), whichever should take least.  Against
 // the best of the three the rule lost 0.5% in the mean over 42 sizes from 40 x 1024 x 512 to 3000 x 5120 x 1536.
-e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, cudaStream_t s) {
+e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, const ColumnSums& sums, cudaStream_t s) {
   if (count > 1 && count <= kMultiMax) {
     double apart = 0.0;
     for (int i = 0; i < count; ++i)
       apart += 8.0 + (g[i].a_mn ? choose<true, true, kEpiLinear>(g[i]) : choose<false, true, kEpiLinear>(g[i])).time;
+    if (sums.out_a || sums.out_b) apart += 8.0;
     MultiParams small = {}, pairs = {};
+    small.sums = pairs.sums = sums;
     const double t1 = plan_multi<1>(g, count, small), t2 = plan_multi<2>(g, count, pairs);
     if (t1 < t2 && t1 < apart) return launch_multi<1>(g, small, s);
     if (t2 < apart) return launch_multi<2>(g, pairs, s);
@@ -1302,7 +1343,7 @@ e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, cudaStream_t 
     const e4b_status st = launch_dense_gemm(g[i], s);
     if (st != E4B_OK) return st;
   }
-  return E4B_OK;
+  return launch_column_sums(sums, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
 
 }  // namespace e4b

@@ -229,11 +229,19 @@ cudaError_t launch_rmsnorm_backward(const NormBackwardLaunch& p, cudaStream_t s)
 
 // out[n] = sum over rows of in[., n] (fp32, fixed order).
 cudaError_t launch_column_sum(const float* in, int rows, int N, float* out, cudaStream_t s);
-// Two of them in one launch, either left out by a null `out`: of the fp32 rows a, and of the bf16 rows b (Nb even,
-// 4-byte aligned).  partial: [column_sum_splits(rows_b), Nb] fp32, 8-byte aligned.
+// Two of them in one launch, either left out by a null `out`: of the fp32 rows a (Na a multiple of 8, 32-byte
+// aligned), and of the bf16 rows b (Nb a multiple of 8, 16-byte aligned).
+struct ColumnSums {
+  const float* a;
+  int32_t rows_a, Na;
+  float* out_a;
+  const uint16_t* b;
+  int32_t rows_b, Nb;
+  float* partial;             // [column_sum_splits(rows_b), Nb], 8-byte aligned
+  float* out_b;
+};
 int column_sum_splits(int rows);
-cudaError_t launch_column_sums(const float* a, int rows_a, int Na, float* out_a, const uint16_t* b, int rows_b, int Nb,
-                               float* partial, float* out_b, cudaStream_t s);
+cudaError_t launch_column_sums(const ColumnSums& c, cudaStream_t s);
 
 // Gradient norm and clipping; partial holds grad_norm_partials(tensors) doubles.
 size_t grad_norm_partials(int32_t tensors);
@@ -264,8 +272,8 @@ struct DenseGemmLaunch {
 };
 inline size_t dense_colsum_rows(int32_t M) { return (static_cast<size_t>(M) + 127) / 128 * 8; }
 e4b_status launch_dense_gemm(const DenseGemmLaunch& g, cudaStream_t s);
-// Up to three kEpiLinear products without bias or addition that do not depend on one another.
-e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, cudaStream_t s);
+// Up to three kEpiLinear products without bias or addition that do not depend on one another, and the column sums.
+e4b_status launch_dense_group(const DenseGemmLaunch* g, int count, const ColumnSums& sums, cudaStream_t s);
 
 // The same products for at most 32 tokens, bound by the weight stream (dense_decode_takes says for which).  The down
 // launch (gate_up false) has to follow the gate_up launch that writes its x directly on the stream.

@@ -98,17 +98,16 @@ int column_sum_splits(int rows) {
   return b < 1 ? 1 : (b > 128 ? 128 : b);
 }
 
-cudaError_t launch_column_sums(const float* a, int rows_a, int Na, float* out_a, const uint16_t* b, int rows_b, int Nb,
-                               float* partial, float* out_b, cudaStream_t s) {
-  const int splits = column_sum_splits(rows_b), per = (rows_b + splits - 1) / splits;
-  const int blocks_a = out_a ? (Na + 31) / 32 : 0, blocks_b = (Nb + 63) / 64;
-  const int grid = blocks_a + (out_b ? blocks_b * splits : 0);
+cudaError_t launch_column_sums(const ColumnSums& c, cudaStream_t s) {
+  const int splits = column_sum_splits(c.rows_b), per = (c.rows_b + splits - 1) / splits;
+  const int blocks_a = c.out_a ? (c.Na + 31) / 32 : 0, blocks_b = (c.Nb + 63) / 64;
+  const int grid = blocks_a + (c.out_b ? blocks_b * splits : 0);
   if (grid == 0) return cudaSuccess;
-  const cudaError_t e = launch_pdl(column_sums_kernel, dim3(grid), dim3(32 * kGroups), 0, s, a, rows_a, Na, out_a,
-                                   blocks_a, reinterpret_cast<const uint32_t*>(b), rows_b, Nb, per, blocks_b,
-                                   splits > 1 ? partial : out_b);
-  if (e != cudaSuccess || !out_b || splits == 1) return e;
-  return launch_column_sum(partial, splits, Nb, out_b, s);
+  const cudaError_t e = launch_pdl(column_sums_kernel, dim3(grid), dim3(32 * kGroups), 0, s, c.a, c.rows_a, c.Na,
+                                   c.out_a, blocks_a, reinterpret_cast<const uint32_t*>(c.b), c.rows_b, c.Nb, per,
+                                   blocks_b, splits > 1 ? c.partial : c.out_b);
+  if (e != cudaSuccess || !c.out_b || splits == 1) return e;
+  return launch_column_sum(c.partial, splits, c.Nb, c.out_b, s);
 }
 
 }  // namespace e4b
