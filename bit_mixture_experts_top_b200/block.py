@@ -57,6 +57,7 @@ class RmsNorm:
         self.H, self.eps = weight.numel(), float(eps)
         self.weight = _check(weight, "weight", (self.H,), torch.bfloat16)
         self.index = weight.get_device()
+        self._ws_bytes = {}                     # backward workspace sizes by rows
 
     def _run(self, x, residual, q_format, want_rstd):
         if x.dim() != 2:
@@ -113,9 +114,14 @@ class RmsNorm:
             _check(dr, "dr", (T, H), torch.bfloat16)
         with _on(self.index, dy, r, rstd, dr):
             dx = torch.empty_like(r)
-            dw = r.new_empty((H,), dtype=torch.float32)
-            ws = r.new_empty(e4b.e4b_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8)
-            e4b.e4b_rmsnorm_backward(dy, e4b.DTYPES[dy.dtype], dr, r, self.weight, rstd, T, H, dx, dw, ws)
+            dw = r.new_empty(H, dtype=torch.float32)
+            nbytes = self._ws_bytes.get(T)
+            if nbytes is None:
+                nbytes = self._ws_bytes[T] = e4b.e4b_rmsnorm_backward_workspace_bytes(T, H)
+            ws = r.new_empty(nbytes, dtype=torch.uint8)
+            e4b._check(e4b.lib().e4b_rmsnorm_backward(
+                dy.data_ptr(), e4b.DTYPES[dy.dtype], _ptr(dr), r.data_ptr(), self.weight.data_ptr(), rstd.data_ptr(), T, H,
+                dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, e4b._stream(None)), "e4b_rmsnorm_backward")
         return dx, dw
 
 
@@ -190,9 +196,9 @@ class GluFfn:
             dx = torch.empty_like(saved.x)
             dgu = torch.empty_like(self.gate_up) if weights else None
             ddn = torch.empty_like(self.down) if weights else None
-            dbg = dout.new_empty((2 * self.I,), dtype=torch.float32) \
+            dbg = dout.new_empty(2 * self.I, dtype=torch.float32) \
                 if weights and self.gu_bias is not None else None
-            dbd = dout.new_empty((self.H,), dtype=torch.float32) \
+            dbd = dout.new_empty(self.H, dtype=torch.float32) \
                 if weights and self.dn_bias is not None else None
             e4b.e4b_ffn_backward(self.desc, T, saved.x, dout, self.gate_up, self.down, dx, dgu, ddn, dbg, dbd, saved.ws)
         return dx, dgu, ddn, dbg, dbd

@@ -42,7 +42,7 @@ def _inputs(T, H, residual=True):
 
 # one value, one word, odd, ragged against the block width, each kernel's range and beyond it
 SHAPES = [(1, 1), (3, 7), (5, 8), (4, 33), (3, 64), (17, 100), (1, 2048), (33, 2056), (7, 2880), (300, 96), (2, 8192),
-          (3, 8200), (2, 32768), (2, 32776), (2, 40001)]
+          (3, 8200), (2, 32768), (2, 32776), (2, 40001), (9, 255), (5, 257), (400, 2883), (3, 8191), (3, 8193)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
@@ -123,6 +123,21 @@ def test_misaligned_rows(shift):
     wr, _, wy = dense.rmsnorm(x, res, w, 1e-6)
     assert np.array_equal(to_np_bits(r), wr)
     assert np.array_equal(to_np_bits(y), bf16.f64_to_bf16_bits(wy.astype(np.float64)))
+
+
+@pytest.mark.parametrize("H", [32, 256, 2880, 8192, 8224])
+def test_misaligned_rows_in_8_bits(H):
+    T = 4
+    x, res, w = _inputs(T, H)
+    x[1, 7], x[2, 31] = 0x7F80, 0x7FC0                     # an infinity, a NaN
+    buf = torch.zeros(T * H + 8, dtype=torch.bfloat16, device=device())
+    xd = buf[3:3 + T * H].view(T, H)
+    xd.copy_(_dev(x))
+    _, _, wy = dense.rmsnorm(x, res, w, 1e-6)
+    for scales, want in (("row", dense.quantize_rows(wy)), ("mx", dense.quantize_mx(wy))):
+        q, s, _ = block.RmsNorm(_dev(w)).forward_q8(xd, _dev(res), scales=scales)
+        assert np.array_equal(q.view(torch.uint8).cpu().numpy(), want[0]), scales
+        assert np.array_equal(s.cpu().numpy(), want[1], equal_nan=scales == "row"), scales
 
 
 @pytest.mark.parametrize("H", [64, 2048, 2056, 4096, 8200, 33])
