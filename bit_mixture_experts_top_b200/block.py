@@ -268,13 +268,14 @@ class GradClipper:
         self._table = ctypes.addressof(self.grads)
         with _on(self.index, *tensors):
             self.ws_bytes = e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads))
+            self._norm_like = tensors[0].new_empty((), dtype=torch.float32)   # (empty_like is torch's cheapest allocation)
 
     def clip(self, max_norm):
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before clipping, a 0-d fp32
         tensor on the device.  max_norm float("inf"): the norm alone."""
         with _on(self.index):
             first = self.grads.tensors[0][0]
-            norm = first.new_empty((), dtype=torch.float32)
+            norm = torch.empty_like(self._norm_like)
             ws = first.new_empty(self.ws_bytes, dtype=torch.uint8)
             e4b._check(e4b.lib().e4b_clip_grad_norm(self._table, len(self.grads), float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                                     self.ws_bytes, e4b._stream(None)), "e4b_clip_grad_norm")
