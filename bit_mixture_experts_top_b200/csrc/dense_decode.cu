@@ -213,11 +213,12 @@ cudaError_t launch_tokens(const DenseDecodeLaunch& p, cudaStream_t s) {
 
 }  // namespace
 
-// Measured against the split tcgen05 kernel: at 32 tokens 7.3 us against 11.2 for 2048 x 768 and 22.2 against 22.5
-// for 2880 x 2880, but 79 against 69 for 4096 x 12288 (each weight byte then meets four token tiles); at 16 tokens
-// it wins at every size.
+// Measured against the tcgen05 kernels: at 17 to 32 tokens 7.3 us against 9.4 for 2048 x 768 and 12.4 against 11.8 for
+// 1536 x 2048, 22.5 against 17.7 for 2880 x 2880 (each weight byte then meets four token tiles); up to 8 tokens it wins
+// at every size (4096 x 12288: 51 against 68), from 9 to 16 at most (10.2 against 13.1 for 2048 x 2048, 60 against 57
+// to 70 for 4096 x 12288).
 bool dense_decode_takes(int32_t T, int32_t H, int32_t I) {
-  return T <= 16 || (T <= 32 && static_cast<int64_t>(H) * I <= (int64_t(1) << 23));
+  return T <= 16 || (T <= 32 && static_cast<int64_t>(H) * I <= (int64_t(1) << 21));
 }
 
 cudaError_t launch_dense_decode(const DenseDecodeLaunch& p, bool gate_up, cudaStream_t s) {
