@@ -863,7 +863,8 @@ static e4b_status check_grads(const e4b_grad* g, int32_t tensors, const Range& n
   if (!std::is_sorted(outs, outs + n, before)) std::sort(outs, outs + n, before);
   for (int32_t i = 1; i < n; ++i)
     if (outs[i].r.lo < outs[i - 1].r.hi) st = E4B_ERR_INVALID_ARG;
-  // the outs are now in order and apart: a grad can only overlap those around it
+  // the outs are now in order and apart: a grad can only overlap those around it, and none of them where the grads
+  // are the outs or lie apart from all of them
   auto clash = [&](const Range& r, int32_t own) {
     const Span key{r, 0};
     const Span* it = std::upper_bound(outs, outs + n, key, before);
@@ -871,11 +872,19 @@ static e4b_status check_grads(const e4b_grad* g, int32_t tensors, const Range& n
       if (overlap(s->r, r) && !(s->owner == own && s->r.lo == r.lo)) return true;
     return false;
   };
+  Range all{~uintptr_t(0), 0};
+  bool in_place = true;
   for (int32_t i = 0; i < tensors && st == E4B_OK; ++i)
     if (g[i].n > 0) {
       const Range r = range_of(g[i].grad, bytes(i));
-      if (clash(r, i) || overlap(r, norm) || overlap(r, ws)) st = E4B_ERR_INVALID_ARG;
+      if (r.lo < all.lo) all.lo = r.lo;
+      if (r.hi > all.hi) all.hi = r.hi;
+      in_place = in_place && g[i].grad == g[i].out;
+      if (overlap(r, norm) || overlap(r, ws)) st = E4B_ERR_INVALID_ARG;
     }
+  if (st == E4B_OK && n > 0 && !in_place && overlap(all, Range{outs[0].r.lo, outs[n - 1].r.hi}))
+    for (int32_t i = 0; i < tensors && st == E4B_OK; ++i)
+      if (g[i].n > 0 && clash(range_of(g[i].grad, bytes(i)), i)) st = E4B_ERR_INVALID_ARG;
   if (st == E4B_OK && (clash(norm, -1) || clash(ws, -1) || overlap(norm, ws))) st = E4B_ERR_INVALID_ARG;
   delete[] outs;
   return st;

@@ -35,7 +35,7 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kSmall = 64, kMedium = 256, kMaxTable = 960;   // 2, 8 and 30 KB of kernel arguments
+constexpr int kSmall = 64, kMedium = 384, kMaxTable = 960;   // 2, 12 and 30 KB of kernel arguments
 constexpr int kBlocksPerSm = 8;
 constexpr int kNormWords = 4, kScaleWords = 2, kLongWords = 8;   // 16-byte words per thread and chunk
 constexpr size_t kLongBytes = size_t(160) << 20;   // a launch's tensors from which on chunks are long and strided
@@ -340,14 +340,16 @@ struct ClipRun {
     ClipTable<N> t;
     fill_table(t, g, count, LONG ? kLongWords : kNormWords);
     *blocks = norm_blocks(t.chunks);
-    return launch_pdl(grad_norm_kernel<N, LONG>, dim3(*blocks), dim3(kThreads), 0, s, t, partial);
+    void* args[] = {&t, &partial};
+    return launch_pdl_args(reinterpret_cast<const void*>(grad_norm_kernel<N, LONG>), dim3(*blocks), dim3(kThreads), s, args);
   }
   template <int N, bool LONG>
   cudaError_t scale(const double* partial, int partials, double max_norm, float* total_norm) const {
     ClipTable<N> t;
     fill_table(t, g, count, LONG ? kLongWords : kScaleWords);
-    return launch_pdl(grad_scale_kernel<N, LONG>, dim3(scale_blocks(t.chunks, LONG)), dim3(kThreads), 0, s, t, partial,
-                      partials, max_norm, total_norm);
+    void* args[] = {&t, &partial, &partials, &max_norm, &total_norm};
+    return launch_pdl_args(reinterpret_cast<const void*>(grad_scale_kernel<N, LONG>), dim3(scale_blocks(t.chunks, LONG)),
+                           dim3(kThreads), s, args);
   }
   cudaError_t norm(double* partial, int* blocks) const {
     if (count <= kSmall) return is_long ? norm<kSmall, true>(partial, blocks) : norm<kSmall, false>(partial, blocks);
