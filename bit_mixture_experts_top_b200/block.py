@@ -221,27 +221,28 @@ class MoeBlock:
     def forward(self, x, residual=None):
         """(out [T, H], r [T, H]): the experts' output and the stream x + residual that it is added to next."""
         y, r = self.norm.forward(x, residual)
-        out = self.moe.forward(y, self._logits(y))
+        out = self.moe.forward(y, self._logits(y), ws=self.moe.new_workspace(len(y), y.device))
         return (out if self.shared is None else self.shared.forward(y, add=out, out=out)), r
 
     def forward_train(self, x, residual=None):
-        """(out, r, saved): the forward with what :meth:`backward` needs.  The routed layer keeps its part in its own
-        workspace, so each forward_train is followed by its backward before the next."""
+        """(out, r, saved): the forward with what :meth:`backward` needs, the routed layer's workspace among it, so other
+        calls may come between a forward_train and its backward."""
         y, r, rstd = self.norm.forward_train(x, residual)
         logits = self._logits(y)
-        out = self.moe.forward_train(y, logits)
+        ws = self.moe.new_workspace(len(y), y.device, train=True)
+        out = self.moe.forward_train(y, logits, ws=ws)
         kept = None
         if self.shared is not None:
             out, kept = self.shared.forward_train(y, add=out, out=out)
-        return out, r, (y, r, rstd, logits, kept)
+        return out, r, (y, r, rstd, logits, kept, ws)
 
     def backward(self, saved, dout, dr=None, router_grad=None, weights=True):
         """Gradients of sum(dout * out) + sum(dr * r) as a dict: dx [T, H] bf16 (of x and residual alike), norm [H]
         fp32, dlogits [T, E] fp32, lora_A / lora_B fp32 (None without LoRA) and, with a shared expert, gate_up, down,
         gu_bias and dn_bias (None where frozen or absent).  router_grad: a callable dlogits -> its part of dy [T, H],
         the router's own backward; None leaves the router's path out of dx."""
-        y, r, rstd, logits, kept = saved
-        dy, dlogits, dA, dB = self.moe.backward(logits, dout)
+        y, r, rstd, logits, kept, ws = saved
+        dy, dlogits, dA, dB = self.moe.backward(logits, dout, ws=ws)
         got = dict(dlogits=dlogits, lora_A=dA, lora_B=dB)
         if self.shared is not None:
             dys, *rest = self.shared.backward(kept, dout, weights)

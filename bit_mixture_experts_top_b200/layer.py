@@ -49,6 +49,7 @@ class MoeLayer:
         self.lora_scale = lora_scale
         self.desc = e4b.make_desc(E, H, I, k, fmt, self.lora_rank, lora_scale, tokens_per_tile, glu, gating)
         self._ws = None
+        self._ws_bytes = {}                     # workspace sizes by (tokens, training)
 
     def workspace(self, T, device):
         need = e4b.e4b_moe_workspace_bytes(self.desc, T)
@@ -58,13 +59,25 @@ class MoeLayer:
             self._ws = torch.empty(need, dtype=torch.uint8, device=device)
         return self._ws
 
+    def new_workspace(self, T, device, train=False):
+        """A workspace for T tokens that the layer does not keep: what forward_train leaves for backward stays in it."""
+        nbytes = self._ws_bytes.get((T, train))
+        if nbytes is None:
+            query = e4b.e4b_moe_train_workspace_bytes if train else e4b.e4b_moe_workspace_bytes
+            nbytes = self._ws_bytes[T, train] = query(self.desc, T)
+        if nbytes == 0:
+            raise ValueError("e4b: unsupported layer shape")
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
     def forward(self, x_bits: torch.Tensor, logits_bits: torch.Tensor, out: Optional[torch.Tensor] = None,
-                stream=None):
-        """x: [T, H] bf16 bits (int16/uint16/bf16 tensor), logits: [T, E].  Returns out [T, H] (bf16)."""
+                stream=None, ws: Optional[torch.Tensor] = None):
+        """x: [T, H] bf16 bits (int16/uint16/bf16 tensor), logits: [T, E].  Returns out [T, H] (bf16).
+        ws: a workspace of the caller's own (see :meth:`new_workspace`); None takes the layer's, which all of its
+        calls without one share: they have to follow one another, and a call with more tokens replaces it."""
         T = x_bits.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x_bits.device)
-        ws = self.workspace(T, x_bits.device)
+        ws = self.workspace(T, x_bits.device) if ws is None else ws
         e4b.e4b_moe_forward(self.desc, T, x_bits, logits_bits, self.gate_up.codes, self.gate_up.scales,
                             self.down.codes, self.down.scales, self.lora_A, self.lora_B, self.gu_bias, self.dn_bias,
                             out, ws, stream)
@@ -78,20 +91,20 @@ class MoeLayer:
             self._ws = torch.empty(need, dtype=torch.uint8, device=device)
         return self._ws
 
-    def forward_train(self, x_bits, logits_bits, out=None, stream=None):
-        """The forward, keeping in the workspace what :meth:`backward` needs."""
+    def forward_train(self, x_bits, logits_bits, out=None, stream=None, ws=None):
+        """The forward, keeping in the workspace (ws, or the layer's own) what :meth:`backward` needs."""
         T = x_bits.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x_bits.device)
-        ws = self.train_workspace(T, x_bits.device)
+        ws = self.train_workspace(T, x_bits.device) if ws is None else ws
         e4b.e4b_moe_forward_train(self.desc, T, x_bits, logits_bits, self.gate_up.codes, self.gate_up.scales,
                                   self.down.codes, self.down.scales, self.lora_A, self.lora_B, self.gu_bias,
                                   self.dn_bias, out, ws, stream)
         return out
 
-    def backward(self, logits_bits, dout_bits, stream=None):
+    def backward(self, logits_bits, dout_bits, stream=None, ws=None):
         """Gradients (dx [T, H], dlogits [T, E], dA [E, H, r], dB [E, r, 2I], fp32) of sum(dout * out) for the
-        last :meth:`forward_train`; dA, dB are None without LoRA."""
+        last :meth:`forward_train` on the workspace ws (None: the layer's own); dA, dB are None without LoRA."""
         T = logits_bits.shape[0]
         dev = logits_bits.device
         dx = torch.empty((T, self.H), dtype=torch.float32, device=dev)
@@ -101,8 +114,8 @@ class MoeLayer:
             dA = torch.empty((self.E, self.H, self.lora_rank), dtype=torch.float32, device=dev)
             dB = torch.empty((self.E, self.lora_rank, 2 * self.I), dtype=torch.float32, device=dev)
         e4b.e4b_moe_backward(self.desc, T, logits_bits, dout_bits, self.gate_up.codes, self.gate_up.scales,
-                             self.down.codes, self.down.scales, self.lora_A, self.lora_B, dx, dl, dA, dB, self._ws,
-                             stream)
+                             self.down.codes, self.down.scales, self.lora_A, self.lora_B, dx, dl, dA, dB,
+                             self._ws if ws is None else ws, stream)
         return dx, dl, dA, dB
 
     def region(self, T, which, dtype):
