@@ -38,13 +38,15 @@ constexpr int BK = 64;                   // K per stage: one 128-byte swizzle ro
 constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, EPI_WARPS = 16;
 constexpr int THREADS = 32 * (WARP_EPI0 + EPI_WARPS);
 constexpr uint64_t kDrainNs = 50000000ull;
-// The tensor cores truncate each step's fp32 sum, so a long accumulation ends
-// short of its value: by 0.75e-9 to 1.1e-9 of it per product, measured over K of
-// 256 to 12288 on zero-mean and on positive data.  Where an fp32 result leaves
-// the kernel (G, and through it and dh the bias gradients) the mean loss is put
-// back; at K = 2048 the error of G falls from 2.1e-6 to 1.1e-6, on positive data
-// to 0.3e-6.  The bf16 results do not see it.
-constexpr float kTruncation = 0.95e-9f;
+// The tensor cores truncate each step's fp32 sum, so a long accumulation of
+// values that do not add up exactly ends short of its sum: by 0.75e-9 to 1.1e-9
+// of it per product, measured over K of 256 to 12288 on zero-mean and on positive
+// data.  Nothing is put back: a factor would be wrong for every sum that was
+// exact (a gate exactly on the clamp would fall outside).  The split kernel, whose
+// tensor memory has room, lets several short chains meet in rounded additions
+// where an fp32 result leaves the kernel; the tiled kernels, whose two accumulators
+// fill the tensor memory, keep one chain (bias gradients 2.6e-6 off at 1500 tokens,
+// 4.3e-6 at 4096 with K = 2048, 6.1e-6 at 3000 with K = 2880).
 constexpr int kGroupM = 16;              // row tiles that share a sweep over the columns (L2 reuse of both operands)
 
 template <int BN, int CG>
@@ -67,7 +69,6 @@ struct Params {
   int32_t m_tiles, n_tiles;
   int32_t act;
   float alpha, limit, beta;
-  float regain;             // gate_up, dact: 1 + kTruncation * (products in one accumulation chain)
   const float* bias;        // gate_up: [2I]; linear: [N]; or null
   int32_t bias_words;       // bias is 16-byte aligned
   const uint16_t* add;      // linear: [M, N] bf16 or null
@@ -277,9 +278,9 @@ __device__ __forceinline__ void finish_dact(const Params& p, int row, bool row_i
   }
 }
 
-__device__ __forceinline__ void take8(const uint32_t (&r)[16], int j, float (&f)[8], float scale = 1.0f) {
+__device__ __forceinline__ void take8(const uint32_t (&r)[16], int j, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[j + i]) * scale;
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[j + i]);
 }
 
 template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
@@ -468,11 +469,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = 0; j < 2; ++j) {
           if (j == 1 && !both) break;
           float f[8];
-          if constexpr (EPI == kEpiLinear) take8(r, 8 * j, f);
-          else take8(r, 8 * j, f, p.regain);
+          take8(r, 8 * j, f);
           if constexpr (EPI == kEpiGateUp) {
             float fu[8];
-            take8(u, 8 * j, fu, p.regain);
+            take8(u, 8 * j, fu);
             v[j] = finish_gate_up(p, row, row_in, col + 8 * j, f, fu);
           } else if constexpr (EPI == kEpiLinear) {
             v[j] = finish_linear(p, row, row_in, col + 8 * j, f);
@@ -528,6 +528,11 @@ struct SplitCfg {
   static constexpr int OFF_MISC = OFF_BAR + (2 * MAX_STAGES + 1) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int EPI = 8, THREADS = 32 * (WARP_EPI0 + EPI);
+  // G and dh, whose fp32 values are kept or summed up, are accumulated in four chains of a quarter of the CTA's K,
+  // added in fp32 with rounding: the gate and up bias gradients of 509 x 2048 x 768 are 3.8e-7 off instead of 1.5e-6
+  // (relative 2-norm), for no more time.  What leaves as bf16 alone does not see it.
+  template <int E>
+  static constexpr int chains() { return E == kEpiLinear ? 1 : 4; }
   static_assert(OFF_SUMS + EPI * 2 * BN * 4 <= RING_BYTES, "both reuse the stages");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -557,6 +562,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     dense_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                        const Params p, int S) {
   using C = SplitCfg;
+  constexpr int CHAINS = C::chains<EPI>();
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     tma_prefetch_desc(&tm_b);
   }
   if (warp == WARP_MMA) {      // (no other tensor-memory kernel of the library leaves room for this one on its SM)
-    tmem_alloc(s_tmem, C::BN);
+    tmem_alloc(s_tmem, CHAINS * C::BN);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -598,6 +604,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
   const int steps = (p.K + C::SK - 1) / C::SK;
   const int first = static_cast<int>(static_cast<int64_t>(steps) * rank / S);
   const int last = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / S);      // S <= steps: never empty
+  const int per_chain = (last - first + CHAINS - 1) / CHAINS;
   auto atoms_of = [&](int ks) { return min(2, (p.K - ks * C::SK + BK - 1) / BK); };
 
   if (warp == WARP_TMA) {
@@ -659,8 +666,8 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     const uint64_t da0 = A_MN ? smem_desc_mn_sw128(base) : smem_desc_sw128(base);
     const uint64_t db0 = B_MN ? smem_desc_mn_sw128(base + 2 * a_atom) : smem_desc_sw128(base + 2 * a_atom);
     constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
-    int stage = 0;
-    uint32_t phase = 0;
+    int stage = 0, in_chain = 0;
+    uint32_t phase = 0, d = tmem_base;
     bool ok = true, issued = false;
     pdl_wait();
     if (p.clear_status && blockIdx.x == 0 && lane < 2) p.status[lane] = 0;
@@ -673,15 +680,16 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < C::SK / 16; ++kk) {
           if (kk >= 4 * atoms) break;
-          umma_bf16_ss(tmem_base, da + static_cast<uint32_t>((kk >> 2) * (a_atom >> 4) + (kk & 3) * a_step),
+          umma_bf16_ss(d, da + static_cast<uint32_t>((kk >> 2) * (a_atom >> 4) + (kk & 3) * a_step),
                        db + (kk >> 2) * (C::ATOM >> 4) + (kk & 3) * b_step, idesc,
-                       (ks > first || kk > 0) ? 1u : 0u);
+                       (in_chain > 0 || kk > 0) ? 1u : 0u);
         }
         umma_commit(&empty[stage]);
         if (ks == last - 1) umma_commit(acc_full);
       }
       __syncwarp();
       issued = true;
+      if (++in_chain == per_chain) { in_chain = 0; d += C::BN; }
       if (++stage == stages) { stage = 0; phase ^= 1u; }
     }
     if (!ok && issued && lane == 0)
@@ -696,10 +704,24 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
       if (m0 + 32 * q < p.M) {
 #pragma unroll
         for (int c0 = half * (C::BN / 2); c0 < (half + 1) * (C::BN / 2); c0 += 32) {
+          const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0;
           uint32_t r[16], u[16];
-          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
-          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0 + 16, u);
+          tmem_ld_32x32b_x16(at, r);
+          tmem_ld_32x32b_x16(at + 16, u);
           tmem_ld_wait();
+          if constexpr (CHAINS > 1) {
+            for (int c = 1; c * per_chain < last - first; ++c) {
+              uint32_t v[16], w[16];
+              tmem_ld_32x32b_x16(at + c * C::BN, v);
+              tmem_ld_32x32b_x16(at + c * C::BN + 16, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(v[j]));
+                u[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(w[j]));
+              }
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             *reinterpret_cast<uint4*>(row + c0 + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
@@ -747,7 +769,6 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
         if (r >= rows) break;
         const int64_t row = m0 + r;
         float4 f = sum[i];
-        if constexpr (EPI != kEpiLinear) f = make_float4(f.x * p.regain, f.y * p.regain, f.z * p.regain, f.w * p.regain);
         if constexpr (EPI != kEpiDact) add4(f, bias);
         if constexpr (EPI == kEpiGateUp) {             // lanes 0..15 hold gate, 16..31 the matching up features
           if (p.g_out && col_in)
@@ -812,7 +833,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
   cluster_sync();                                 // the partial tile stays until every rank has read it
   if (warp == WARP_MMA) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, C::BN);
+    tmem_dealloc(tmem_base, CHAINS * C::BN);
   }
 }
 
@@ -1100,7 +1121,7 @@ bool encode_operands(const DenseGemmLaunch& g, int b_box, CUtensorMap* ta, CUten
   return enc(ta, g.a, g.M, g.K, A_MN, a_box) && enc(tb, g.b, b_rows, g.K, B_MN, b_box);
 }
 
-Params make_params(const DenseGemmLaunch& g, int tile_rows, int width, int tile_cols, int split = 1) {
+Params make_params(const DenseGemmLaunch& g, int tile_rows, int width, int tile_cols) {
   Params p;
   p.M = g.M;
   p.N = g.N;
@@ -1112,7 +1133,6 @@ Params make_params(const DenseGemmLaunch& g, int tile_rows, int width, int tile_
   p.alpha = g.alpha;
   p.limit = g.limit;
   p.beta = g.beta;
-  p.regain = 1.0f + kTruncation * static_cast<float>(g.K / split);
   p.bias = g.bias;
   p.bias_words = aligned(g.bias, 16) ? 1 : 0;
   p.add = g.add;
@@ -1178,7 +1198,7 @@ e4b_status launch_split(const DenseGemmLaunch& g, int S, cudaStream_t s) {
   constexpr int NT = EPI == kEpiGateUp ? SplitCfg::BN / 2 : SplitCfg::BN;
   CUtensorMap ta, tb;
   if (!encode_operands<A_MN, B_MN, EPI>(g, NT, &ta, &tb, g.M <= BM / 2 ? BM / 2 : BM)) return E4B_ERR_CUDA;
-  const Params p = make_params(g, BM, SplitCfg::BN, NT, S);
+  const Params p = make_params(g, BM, SplitCfg::BN, NT);
   if (g.colsum_rows) *g.colsum_rows = p.m_tiles * S;
   const dim3 grid(static_cast<unsigned>(p.m_tiles * p.n_tiles * S));
   return launch_pdl_cluster(static_cast<unsigned>(S), dense_split_kernel<A_MN, B_MN, EPI>, grid, dim3(SplitCfg::THREADS),
