@@ -257,25 +257,38 @@ class MoeBlock:
 class GradClipper:
     """Clipping of a fixed list of gradient tensors (fp32, bf16 and fp16 mixed, each contiguous) by their global norm.
 
-    The list is described once and its tensors are held; every :meth:`clip` reads them anew."""
+    The list is described once and its tensors are held; every :meth:`clip` reads them anew.  A tensor that has been
+    given other storage since (``t.data = ...``, ``set_``, a ``resize_`` that moved it) is described again; on storage
+    that it keeps, a tensor has to keep its type and size too."""
 
     def __init__(self, grads, out=None):
         """out: tensors of the same types and sizes that take the clipped values; None clips in place."""
-        self.grads = e4b.make_grads(grads, out)
-        tensors = [t for ts in self.grads.tensors for t in ts]
+        self._describe(grads, out)
+
+    def _describe(self, grads, out):
+        table = e4b.make_grads(grads, out)
+        grads, outs = table.tensors
+        tensors = grads if outs is grads else grads + outs
         if not tensors:
             raise ValueError("e4b: no gradient tensors")
-        self.index = tensors[0].get_device()
-        self._table = ctypes.addressof(self.grads)
-        with _on(self.index, *tensors):
-            self.ws_bytes = e4b.e4b_clip_grad_norm_workspace_bytes(len(self.grads))
+        index = tensors[0].get_device()
+        with _on(index, *tensors):
+            self.ws_bytes = e4b.e4b_clip_grad_norm_workspace_bytes(len(table))
             self._norm_like = tensors[0].new_empty((), dtype=torch.float32)   # (empty_like is torch's cheapest allocation)
+        self.grads, self.index, self._tensors = table, index, tensors
+        self._table = ctypes.addressof(table)
+        # the storages are held with the addresses: nothing else can come to lie there before the next look at them
+        self._storages = [t.untyped_storage() for t in tensors]
+        self._addresses = list(map(torch.Tensor.data_ptr, tensors))
 
     def clip(self, max_norm):
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before clipping, a 0-d fp32
         tensor on the device.  max_norm float("inf"): the norm alone."""
+        if list(map(torch.Tensor.data_ptr, self._tensors)) != self._addresses:
+            grads, outs = self.grads.tensors
+            self._describe(grads, None if outs is grads else outs)
         with _on(self.index):
-            first = self.grads.tensors[0][0]
+            first = self._tensors[0]
             norm = torch.empty_like(self._norm_like)
             ws = first.new_empty(self.ws_bytes, dtype=torch.uint8)
             e4b._check(e4b.lib().e4b_clip_grad_norm(self._table, len(self.grads), float(max_norm), norm.data_ptr(), ws.data_ptr(),
