@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tile_at(p, tile, mt, nt);
       const int buf = it & 1;
       const uint32_t aphase = (it >> 1) & 1;
-      if (!mbar_wait_sleep(&acc_full[buf], aphase, wctx, 1401, 64)) break;
+      if (!__all_sync(kFull, mbar_wait_sleep(&acc_full[buf], aphase, wctx, 1401, 64))) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN);
       const int row0 = (mt * CG + static_cast<int>(rank)) * BM + 32 * q;
