@@ -10,6 +10,10 @@ shared expert in their order, forward and backward) and :class:`GradClipper`
 Every call runs on the current stream of the tensors' device.  Outputs and
 workspaces are allocated per call from torch's allocator, so calls on several
 streams, and calls captured into several graphs, share nothing.
+
+The kernels' waits are bounded.  One that runs out (a device fault or a bug: the
+limit is seconds) leaves outputs that are not to be trusted; :func:`check_waits`
+raises then.
 """
 import contextlib
 import ctypes
@@ -44,6 +48,13 @@ def _on(index, *tensors):
         if t is not None and t.get_device() != index:
             raise ValueError(f"e4b: a tensor on {t.device} in a call on cuda:{index}")
     return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
+def check_waits(device=None):
+    """Synchronises the device's current stream and raises E4BError if a bounded wait of any call on that device, graph
+    replays among them, has run out since the last check: what those calls wrote is not to be trusted."""
+    with torch.cuda.device(device):
+        e4b._check(e4b.e4b_wait_status(), "e4b_wait_status")
 
 
 class RmsNorm:

@@ -24,6 +24,24 @@ int device_sm_count() {
   return n;
 }
 
+// (function-local, so that it is there for whichever source file registers first)
+struct WaitFlags {
+  cudaError_t (*address[32])(void**);
+  int count;
+};
+
+static WaitFlags& wait_flags() {
+  static WaitFlags f = {};
+  return f;
+}
+
+bool register_wait_flag(cudaError_t (*address)(void**)) {
+  WaitFlags& f = wait_flags();
+  if (f.count == 32) return false;
+  f.address[f.count++] = address;
+  return true;
+}
+
 namespace {
 
 __global__ void wait_timeout_probe_kernel(int32_t* status, uint64_t limit_ns) {
@@ -920,6 +938,22 @@ e4b_status e4b_device_status(void* ws, e4b_stream stream) {
   if (cudaMemcpy(h, ws, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return E4B_ERR_CUDA;
   if (h[0] != 0 && cudaMemset(ws, 0, sizeof(h)) != cudaSuccess) return E4B_ERR_CUDA;
   return static_cast<e4b_status>(h[0]);
+}
+
+e4b_status e4b_wait_status(e4b_stream stream) {
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return E4B_ERR_CUDA;
+  e4b_status st = E4B_OK;
+  const WaitFlags& f = wait_flags();
+  for (int i = 0; i < f.count; ++i) {
+    void* p = nullptr;
+    int32_t v = 0;
+    if (f.address[i](&p) != cudaSuccess || cudaMemcpy(&v, p, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return E4B_ERR_CUDA;
+    if (v == 0) continue;
+    if (cudaMemset(p, 0, sizeof(v)) != cudaSuccess) return E4B_ERR_CUDA;
+    st = static_cast<e4b_status>(v);
+  }
+  return st;
 }
 
 e4b_status e4b_debug_wait_timeout(uint32_t limit_ns, void* ws, size_t ws_bytes, e4b_stream stream) {

@@ -6,14 +6,25 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 #include "e4b.h"
 #include "e4b_internal.h"
 
 namespace e4b {
 
-// Device status word: status[0] = first error code, status[1] = where it happened.
-__device__ __forceinline__ void record_error(int32_t* status, int32_t code, int32_t where) {
+// Beside the workspace's status word, which the workspace's next call clears and which is gone with the workspace: set
+// by any kernel of this source file whose wait ran out, until e4b_wait_status reads it.
+static __device__ int32_t wait_ran_out;
+
+static cudaError_t wait_ran_out_address(void** p) { return cudaGetSymbolAddress(p, wait_ran_out); }
+
+static const bool wait_flag_registered = register_wait_flag(wait_ran_out_address);
+
+// Device status word: status[0] = first error code, status[1] = where it happened.  (Out of line: inlined into every wait
+// the two records cost the decoding warps of the grouped kernel 1.6%.)
+static __device__ __noinline__ void record_error(int32_t* status, int32_t code, int32_t where) {
+  atomicExch(&wait_ran_out, code);
   if (atomicCAS(status, 0, code) == 0) {
     atomicExch(status + 1, where);
   }

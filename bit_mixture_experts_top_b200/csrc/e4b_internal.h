@@ -102,6 +102,10 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
+// Each source file with device code has a flag of its own that its kernels set when a wait ran out; `address` gives its
+// address on the current device.
+bool register_wait_flag(cudaError_t (*address)(void**));
+
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // 16 fp32 NF4 levels and the 15 fp32 decision midpoints, built on the host from

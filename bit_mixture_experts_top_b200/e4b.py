@@ -145,6 +145,7 @@ _SIGS = {
     "e4b_clip_grad_norm_workspace_bytes": ([_i32], _sz),
     "e4b_clip_grad_norm": ([_vp, _i32, _f64, _vp, _vp, _sz, _vp], _i32),
     "e4b_device_status": ([_vp, _vp], _i32),
+    "e4b_wait_status": ([_vp], _i32),
     "e4b_debug_wait_timeout": ([_u32, _vp, _sz, _vp], _i32),
 }
 
@@ -369,6 +370,12 @@ def e4b_clip_grad_norm(grads, max_norm, total_norm, ws, stream=None):
 def e4b_device_status(ws, stream=None):
     """Synchronises the stream and returns (and clears) the workspace's device status code."""
     return lib().e4b_device_status(_ptr(ws), _stream(stream))
+
+
+def e4b_wait_status(stream=None):
+    """Synchronises the stream and returns (and clears) E4B_ERR_TIMEOUT if a wait of any call on the current device has
+    run out since the last call of this function, E4B_OK otherwise; needs no workspace."""
+    return lib().e4b_wait_status(_stream(stream))
 
 
 def e4b_debug_wait_timeout(limit_ns, ws, stream=None):

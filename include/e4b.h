@@ -37,7 +37,8 @@
  *     and return E4B_ERR_INVALID_ARG or E4B_ERR_UNSUPPORTED; nothing is
  *     enqueued then.  A failed launch returns E4B_ERR_CUDA.  Kernels never
  *     trap: a bounded wait that runs out records E4B_ERR_TIMEOUT in the
- *     workspace status word, which e4b_device_status() reports.
+ *     workspace status word, which e4b_device_status() reports, and in the
+ *     library, whose e4b_wait_status() reports it for all calls on a device.
  *   - There is no fallback path: a call either runs these kernels or fails.
  *
  * Storage layouts (readings of the pages where they are silent):
@@ -546,6 +547,16 @@ e4b_status e4b_moe_workspace_region(const e4b_moe_desc* d, int32_t T, int32_t re
  * a bounded wait ran out).
  */
 e4b_status e4b_device_status(void* ws, e4b_stream stream);
+
+/*
+ * The same without a workspace, for calls whose workspace has been used again
+ * or freed since: synchronises `stream` and returns E4B_ERR_TIMEOUT if a
+ * bounded wait of any of the library's kernels ran out on the current device
+ * since the last call of this function, E4B_OK otherwise.  The answer covers
+ * the kernels that have ended, on every stream.  Clears what it reports; the
+ * workspaces' own status words stay.  Not inside a stream capture.
+ */
+e4b_status e4b_wait_status(e4b_stream stream);
 
 /*
  * Test hook for the bounded-wait machinery: launches one block that waits on
