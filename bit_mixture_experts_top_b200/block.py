@@ -50,6 +50,18 @@ def _on(index, *tensors):
     return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _lend(stream, index, *tensors):
+    """Tells the allocator that tensors saved on the raw stream `stream` are read on the current one too: dropped right
+    after a backward on another stream, their memory must not be handed out on their own before that backward ends."""
+    if _raw_stream(index) != stream:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(index))
+
+
 def check_waits(device=None):
     """Synchronises the device's current stream and raises E4BError if a bounded wait of any call on that device, graph
     replays among them, has run out since the last check: what those calls wrote is not to be trusted."""
@@ -141,8 +153,8 @@ class FfnSaved:
     before the backward) and the workspace with the pre-activations and h, whose scratch one backward at a time
     uses."""
 
-    def __init__(self, x, ws):
-        self.x, self.ws = x, ws
+    def __init__(self, x, ws, stream):
+        self.x, self.ws, self.stream = x, ws, stream
 
 
 class GluFfn:
@@ -196,7 +208,7 @@ class GluFfn:
     def forward_train(self, x, add=None, out=None):
         """(out, saved): the forward, and what :meth:`backward` needs of it."""
         out, ws = self._run("e4b_ffn_forward_train", e4b.e4b_ffn_train_workspace_bytes, x, add, out)
-        return out, FfnSaved(x, ws)
+        return out, FfnSaved(x, ws, _raw_stream(self.index))
 
     def backward(self, saved, dout, weights=True):
         """(dx, d_gate_up, d_down, d_gu_bias, d_dn_bias) of sum(dout * out): bf16, the biases' fp32 (None without them).
@@ -204,6 +216,7 @@ class GluFfn:
         T = saved.x.shape[0]
         _check(dout, "dout", (T, self.H), torch.bfloat16)
         with _on(self.index, saved.x, dout):
+            _lend(saved.stream, self.index, saved.x, saved.ws)
             dx = torch.empty_like(saved.x)
             dgu = torch.empty_like(self.gate_up) if weights else None
             ddn = torch.empty_like(self.down) if weights else None
@@ -245,14 +258,15 @@ class MoeBlock:
         kept = None
         if self.shared is not None:
             out, kept = self.shared.forward_train(y, add=out, out=out)
-        return out, r, (y, r, rstd, logits, kept, ws)
+        return out, r, (y, r, rstd, logits, kept, ws, _raw_stream(self.norm.index))
 
     def backward(self, saved, dout, dr=None, router_grad=None, weights=True):
         """Gradients of sum(dout * out) + sum(dr * r) as a dict: dx [T, H] bf16 (of x and residual alike), norm [H]
         fp32, dlogits [T, E] fp32, lora_A / lora_B fp32 (None without LoRA) and, with a shared expert, gate_up, down,
         gu_bias and dn_bias (None where frozen or absent).  router_grad: a callable dlogits -> its part of dy [T, H],
         the router's own backward; None leaves the router's path out of dx."""
-        y, r, rstd, logits, kept, ws = saved
+        y, r, rstd, logits, kept, ws, stream = saved
+        _lend(stream, self.norm.index, y, r, rstd, logits, ws)
         dy, dlogits, dA, dB = self.moe.backward(logits, dout, ws=ws)
         got = dict(dlogits=dlogits, lora_A=dA, lora_B=dB)
         if self.shared is not None:

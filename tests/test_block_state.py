@@ -46,6 +46,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(e4b, "e4b_moe_forward_train", forward("train"))
     monkeypatch.setattr(e4b, "e4b_moe_backward", backward)
     monkeypatch.setattr(block, "_check", lambda t, *a: t)
+    monkeypatch.setattr(block, "_raw_stream", lambda index: 0)
     return made
 
 
