@@ -266,6 +266,7 @@ class MoeBlock:
         gu_bias and dn_bias (None where frozen or absent).  router_grad: a callable dlogits -> its part of dy [T, H],
         the router's own backward; None leaves the router's path out of dx."""
         y, r, rstd, logits, kept, ws, stream = saved
+        _check(dout, "dout", y.shape, torch.bfloat16)
         _lend(stream, self.norm.index, y, r, rstd, logits, ws)
         dy, dlogits, dA, dB = self.moe.backward(logits, dout, ws=ws)
         got = dict(dlogits=dlogits, lora_A=dA, lora_B=dB)

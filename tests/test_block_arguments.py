@@ -1,0 +1,49 @@
+"""CPU checks of what block.MoeBlock refuses before the routed layer's entry points get any pointer, with tensors that
+only claim to be on a GPU and entry points that fail the test when they are reached."""
+import contextlib
+
+import pytest
+import torch
+
+from bit_mixture_experts_top_b200 import block, e4b, layer
+from test_block_state import E, H, I, K, FakeNorm
+
+
+class Claims(torch.Tensor):
+    """A CPU tensor that says it is on a GPU."""
+    is_cuda = True
+
+
+def _claims(t):
+    return t.as_subclass(Claims)
+
+
+def _x(T):
+    return _claims(torch.zeros((T, H), dtype=torch.bfloat16))
+
+
+@pytest.fixture
+def blk(monkeypatch):
+    reached = []
+    monkeypatch.setattr(e4b, "e4b_moe_forward_train", lambda *a: None)
+    monkeypatch.setattr(e4b, "e4b_moe_backward", lambda *a: reached.append(a))
+    monkeypatch.setattr(block, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(block, "_on", lambda index, *t: contextlib.nullcontext())
+    stack = lambda n, k: layer.PackedStack(torch.empty(1), torch.empty(1), E, n, k, "nf4")  # noqa: E731
+    moe = layer.MoeLayer(E, H, I, K, "nf4", stack(2 * I, H), stack(H, I))
+    b = block.MoeBlock(FakeNorm(), lambda y: _claims(torch.zeros((len(y), E), dtype=torch.bfloat16)), moe)
+    b.reached = reached
+    return b
+
+
+def test_backward_takes_a_contiguous_gradient_of_the_saved_rows(blk):
+    _, _, saved = blk.forward_train(_x(6))
+    blk.backward(saved, _x(6))
+    assert len(blk.reached) == 1
+    one = _claims(torch.ones((), dtype=torch.bfloat16))
+    for bad in (one.expand(6, H),                            # as a sum's gradient comes: one value, no rows behind it
+                _x(6)[:3], _x(7), _claims(torch.zeros((6, H))), _x(6)[:, : H // 2],
+                _claims(torch.zeros((H, 6), dtype=torch.bfloat16)).t(), torch.zeros((6, H), dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="dout"):
+            blk.backward(saved, bad)
+    assert len(blk.reached) == 1
