@@ -232,33 +232,41 @@ class MoeBlock:
     """The feed-forward half of a block: norm, router, routed 4-bit layer and, where there is one, the shared expert.
 
     norm: :class:`RmsNorm`; moe: :class:`layer.MoeLayer`; shared: :class:`GluFfn` or None; router: a callable
-    y [T, H] -> logits [T, E] (bf16), the model's own projection of the normed rows."""
+    y [T, H] -> logits [T, E] (bf16), the model's own projection of the normed rows.  All parts are on one device, which
+    is the current one while they, the router and its gradient run."""
 
     def __init__(self, norm, router, moe, shared=None):
         if moe.H != norm.H or (shared is not None and shared.H != norm.H):
             raise ValueError("e4b: the norm, the routed layer and the shared expert differ in H")
+        at = {norm.index, moe.gate_up.codes.get_device(), moe.down.codes.get_device()}
+        if len(at if shared is None else at | {shared.index}) != 1:
+            raise ValueError("e4b: the norm, the routed layer and the shared expert are on different devices")
         self.norm, self.router, self.moe, self.shared = norm, router, moe, shared
 
     def _logits(self, y):
-        return _check(self.router(y), "logits", (y.shape[0], self.moe.E), torch.bfloat16)
+        logits = _check(self.router(y), "logits", (y.shape[0], self.moe.E), torch.bfloat16)
+        _on(self.norm.index, logits)             # (the device is the current one already)
+        return logits
 
     def forward(self, x, residual=None):
         """(out [T, H], r [T, H]): the experts' output and the stream x + residual that it is added to next."""
-        y, r = self.norm.forward(x, residual)
-        out = self.moe.forward(y, self._logits(y), ws=self.moe.new_workspace(len(y), y.device))
-        return (out if self.shared is None else self.shared.forward(y, add=out, out=out)), r
+        with _on(self.norm.index, x, residual):
+            y, r = self.norm.forward(x, residual)
+            out = self.moe.forward(y, self._logits(y), ws=self.moe.new_workspace(len(y), y.device))
+            return (out if self.shared is None else self.shared.forward(y, add=out, out=out)), r
 
     def forward_train(self, x, residual=None):
         """(out, r, saved): the forward with what :meth:`backward` needs, the routed layer's workspace among it, so other
         calls may come between a forward_train and its backward."""
-        y, r, rstd = self.norm.forward_train(x, residual)
-        logits = self._logits(y)
-        ws = self.moe.new_workspace(len(y), y.device, train=True)
-        out = self.moe.forward_train(y, logits, ws=ws)
-        kept = None
-        if self.shared is not None:
-            out, kept = self.shared.forward_train(y, add=out, out=out)
-        return out, r, (y, r, rstd, logits, kept, ws, _raw_stream(self.norm.index))
+        with _on(self.norm.index, x, residual):
+            y, r, rstd = self.norm.forward_train(x, residual)
+            logits = self._logits(y)
+            ws = self.moe.new_workspace(len(y), y.device, train=True)
+            out = self.moe.forward_train(y, logits, ws=ws)
+            kept = None
+            if self.shared is not None:
+                out, kept = self.shared.forward_train(y, add=out, out=out)
+            return out, r, (y, r, rstd, logits, kept, ws, _raw_stream(self.norm.index))
 
     def backward(self, saved, dout, dr=None, router_grad=None, weights=True):
         """Gradients of sum(dout * out) + sum(dr * r) as a dict: dx [T, H] bf16 (of x and residual alike), norm [H]
@@ -267,16 +275,17 @@ class MoeBlock:
         the router's own backward; None leaves the router's path out of dx."""
         y, r, rstd, logits, kept, ws, stream = saved
         _check(dout, "dout", y.shape, torch.bfloat16)
-        _lend(stream, self.norm.index, y, r, rstd, logits, ws)
-        dy, dlogits, dA, dB = self.moe.backward(logits, dout, ws=ws)
-        got = dict(dlogits=dlogits, lora_A=dA, lora_B=dB)
-        if self.shared is not None:
-            dys, *rest = self.shared.backward(kept, dout, weights)
-            got.update(zip(("gate_up", "down", "gu_bias", "dn_bias"), rest))
-            dy += dys
-        if router_grad is not None:
-            dy += router_grad(dlogits)
-        got["dx"], got["norm"] = self.norm.backward(dy, r, rstd, dr)
+        with _on(self.norm.index, dout, dr):
+            _lend(stream, self.norm.index, y, r, rstd, logits, ws)
+            dy, dlogits, dA, dB = self.moe.backward(logits, dout, ws=ws)
+            got = dict(dlogits=dlogits, lora_A=dA, lora_B=dB)
+            if self.shared is not None:
+                dys, *rest = self.shared.backward(kept, dout, weights)
+                got.update(zip(("gate_up", "down", "gu_bias", "dn_bias"), rest))
+                dy += dys
+            if router_grad is not None:
+                dy += router_grad(dlogits)
+            got["dx"], got["norm"] = self.norm.backward(dy, r, rstd, dr)
         return got
 
 

@@ -47,3 +47,38 @@ def test_backward_takes_a_contiguous_gradient_of_the_saved_rows(blk):
         with pytest.raises(ValueError, match="dout"):
             blk.backward(saved, bad)
     assert len(blk.reached) == 1
+
+
+def test_every_call_runs_on_the_device_of_the_block(blk, monkeypatch):
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def on(index, *tensors):
+        inside.append((index, [t for t in tensors if t is not None]))
+        yield
+        inside.pop()
+    monkeypatch.setattr(block, "_on", on)
+    for name in ("e4b_moe_forward", "e4b_moe_forward_train", "e4b_moe_backward"):
+        monkeypatch.setattr(e4b, name, lambda *a, name=name: seen.append((name, len(inside))))
+    router, grads = blk.router, lambda dl: seen.append(("router_grad", len(inside))) or torch.zeros((len(dl), H))
+    blk.router = lambda y: seen.append(("router", len(inside))) or router(y)
+    blk.forward(_x(5))
+    _, _, saved = blk.forward_train(_x(5))
+    blk.backward(saved, _x(5), router_grad=grads)
+    assert [n for n, _ in seen] == ["router", "e4b_moe_forward", "router", "e4b_moe_forward_train", "e4b_moe_backward",
+                                    "router_grad"]
+    assert all(depth > 0 for _, depth in seen), seen
+
+
+def test_parts_on_different_devices_are_refused():
+    stack = lambda n, k: layer.PackedStack(torch.empty(1), torch.empty(1), E, n, k, "nf4")  # noqa: E731
+    moe = layer.MoeLayer(E, H, I, K, "nf4", stack(2 * I, H), stack(H, I))
+    elsewhere = FakeNorm()
+    elsewhere.index = 1
+    with pytest.raises(ValueError, match="device"):
+        block.MoeBlock(elsewhere, None, moe)
+
+    class FakeShared:
+        H, index = FakeNorm().H, 1
+    with pytest.raises(ValueError, match="device"):
+        block.MoeBlock(FakeNorm(), None, moe, FakeShared())

@@ -1,6 +1,8 @@
 """CPU checks of what block.MoeBlock keeps between its calls, with the entry points of the routed layer replaced by
 fakes that write their call's number into the workspace: every call has a workspace of its own, and a backward gets
 the one that its own forward filled."""
+import contextlib
+
 import pytest
 import torch
 
@@ -47,6 +49,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(e4b, "e4b_moe_backward", backward)
     monkeypatch.setattr(block, "_check", lambda t, *a: t)
     monkeypatch.setattr(block, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(block, "_on", lambda index, *t: contextlib.nullcontext())
     return made
 
 
