@@ -578,12 +578,15 @@ e4b_status e4b_moe_backward(const e4b_moe_desc* d, int32_t T, const uint16_t* lo
   return launch_moe_backward(b, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// The norm's kernels index a row, and step past its end by a block, in 32 bits.
+static const int32_t kMaxNormSize = 1 << 30;
+
 e4b_status e4b_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
                        double eps, int32_t q_format, uint16_t* r_out, uint16_t* y, uint8_t* q, void* q_scales,
                        float* rstd, e4b_stream stream) {
   if (T < 0 || H < 1 || !(eps >= 0.0) || !std::isfinite(eps)) return E4B_ERR_INVALID_ARG;
   if (q_format != E4B_Q8_NONE && q_format != E4B_Q8_ROW && q_format != E4B_Q8_MX) return E4B_ERR_INVALID_ARG;
-  if (q_format == E4B_Q8_MX && H % 32 != 0) return E4B_ERR_UNSUPPORTED;
+  if (T > kMaxNormSize || H > kMaxNormSize || (q_format == E4B_Q8_MX && H % 32 != 0)) return E4B_ERR_UNSUPPORTED;
   if (T == 0) return E4B_OK;
   const bool quant = q_format != E4B_Q8_NONE;
   if (!x || !weight || (q != nullptr) != quant || (q_scales != nullptr) != quant || (!y && !q) || (r_out && !residual))
@@ -607,7 +610,7 @@ e4b_status e4b_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
 }
 
 size_t e4b_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H) {
-  if (T < 0 || H < 1) return 0;
+  if (T < 0 || H < 1 || T > kMaxNormSize || H > kMaxNormSize) return 0;
   return kStatusBytes + align_up(static_cast<size_t>(norm_backward_blocks(T)) * H * 4);
 }
 
@@ -615,6 +618,7 @@ e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t*
                                 const uint16_t* weight, const float* rstd, int32_t T, int32_t H, uint16_t* dx,
                                 float* dweight, void* ws, size_t ws_bytes, e4b_stream stream) {
   if (T < 0 || H < 1 || (dy_type != E4B_F32 && dy_type != E4B_BF16)) return E4B_ERR_INVALID_ARG;
+  if (T > kMaxNormSize || H > kMaxNormSize) return E4B_ERR_UNSUPPORTED;
   if (!dweight || !aligned(dweight, 4)) return E4B_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) return cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;

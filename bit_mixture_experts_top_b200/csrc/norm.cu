@@ -753,7 +753,7 @@ cudaError_t launch_backward_vec(const NormBackwardLaunch& p, int blocks, cudaStr
 template <typename DY>
 cudaError_t launch_backward_typed(const NormBackwardLaunch& p, bool vec, cudaStream_t s) {
   const int blocks = norm_backward_blocks(p.T);
-  const int row = (static_cast<int>(sizeof(DY)) + (p.dr ? 4 : 2)) * p.H;
+  const int64_t row = static_cast<int64_t>(static_cast<int>(sizeof(DY)) + (p.dr ? 4 : 2)) * p.H;
   cudaError_t e;
   if (vec && p.H <= 16384) {
     if (p.H <= 256) e = launch_backward_vec<DY, 1, 4>(p, blocks, s);

@@ -381,8 +381,9 @@ enum { E4B_Q8_NONE = 0, E4B_Q8_ROW = 1, E4B_Q8_MX = 2 };
  *   rstd     : [T] fp32 or NULL                     (device, written) for the backward
  * One of y and q is required.  r_out or y may be the same buffer as x or
  * residual (in place); any other overlap of an output with another argument
- * is refused.  Any H >= 1 and element alignment are accepted; rows of a multiple
- * of eight values on 16-byte aligned buffers take the fast kernel.
+ * is refused.  Any H from 1 to 2^30, up to 2^30 rows and element alignment are
+ * accepted; rows of a multiple of eight values on 16-byte aligned buffers take
+ * the fast kernel.
  */
 e4b_status e4b_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t T, int32_t H,
                        double eps, int32_t q_format, uint16_t* r_out, uint16_t* y, uint8_t* q, void* q_scales,
