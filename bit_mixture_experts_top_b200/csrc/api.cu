@@ -621,7 +621,14 @@ e4b_status e4b_rmsnorm_backward(const void* dy, int32_t dy_type, const uint16_t*
   if (T > kMaxNormSize || H > kMaxNormSize) return E4B_ERR_UNSUPPORTED;
   if (!dweight || !aligned(dweight, 4)) return E4B_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T == 0) return cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, s) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
+  if (T == 0) {                                      // (a workspace may be left out; one that is there gets its status)
+    const bool has_ws = ws && aligned(ws, kAlign) && ws_bytes >= kStatusBytes;
+    if (has_ws && overlap(range_of(ws, kStatusBytes), range_of(dweight, 4 * static_cast<size_t>(H))))
+      return E4B_ERR_INVALID_ARG;
+    const bool ok = cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, s) == cudaSuccess &&
+                    (!has_ws || cudaMemsetAsync(ws, 0, kStatusBytes, s) == cudaSuccess);
+    return ok ? E4B_OK : E4B_ERR_CUDA;
+  }
   if (!dy || !r || !weight || !rstd || !dx || !ws || !aligned(ws, kAlign)) return E4B_ERR_INVALID_ARG;
   if (!aligned(dy, dy_type == E4B_F32 ? 4 : 2) || !aligned(dr, 2) || !aligned(r, 2) || !aligned(weight, 2) ||
       !aligned(rstd, 4) || !aligned(dx, 2))
