@@ -199,8 +199,11 @@ cudaError_t launch_typed(const DenseDecodeLaunch& p, int grid, cudaStream_t s) {
 
 // Blocks of 64 K in flight per warp.  Up to eight tokens four (two blocks per
 // SM: 5.8 TB/s on 4096 x 12288), but two where that leaves room for the whole
-// grid at once and four does not (2880 x 2880: 13.4 us against 15.3); more
-// tokens need more shared memory per stage and keep two blocks per SM.
+// grid at once and four does not.  One token, us with two / with four: I of 2400
+// to 4704 over H = 1024 6.7 / 8.1, 7.6 / 8.7 (2880), 10.6 / 12.2 (4096), 11.5 / 13.4;
+// H of 4800 to 9400 over I = 1024 9.4 / 10.2, 14.4 / 15.7 (7168), 17.5 / 19.4.  Beside
+// that range two cost as much or more (I = 1600 6.1 / 5.5).  More tokens need more
+// shared memory per stage and keep two blocks per SM.
 template <bool GATE_UP>
 cudaError_t launch_tokens(const DenseDecodeLaunch& p, cudaStream_t s) {
   const int per = GATE_UP ? 8 : 16, grid = (p.N + per - 1) / per, sms = device_sm_count();

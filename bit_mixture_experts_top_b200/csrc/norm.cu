@@ -35,7 +35,11 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kMaxWarps = 32;
 constexpr int kBackThreads = 512, kBackGroups = 15;   // backward: a block's threads, and its groups (one named barrier each)
 constexpr int kSlotBytes = 208 * 1024;                // and the shared memory of its row slots
-constexpr int kManyRowsPerSm = 16;   // from so many rows per SM on, fewer threads take a row
+// From so many rows per SM on, fewer threads take a row of up to 2048 values, one warp up to 1024.  MX output in us, with
+// fewer threads / as for few rows: 1200 x 512 2.6 / 2.5, 2400 x 512 3.1 / 3.9, 2400 x 1024 5.6 / 4.9, 8192 x 1024 11.4 / 12.1,
+// 1200 x 2048 5.5 / 5.1, 2400 x 2048 7.4 / 8.4, 16384 x 2048 37.6 / 44.9.  Wider rows gain nothing (2400 x 2880 10.1 / 9.9,
+// 16384 x 4096 74.3 / 74.0).
+constexpr int kManyRowsPerSm = 16;
 
 __device__ __forceinline__ float bf16_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
@@ -780,16 +784,14 @@ cudaError_t launch_rmsnorm(const NormLaunch& p, cudaStream_t s) {
     if (odd_threads(p.H) <= 1024) return launch_pdl(norm_odd_kernel, dim3(p.T), dim3(odd_threads(p.H)), 0, s, p);
     return launch_pdl(norm_any_kernel, dim3(p.T), dim3(256), 0, s, p);
   }
-  if (p.T >= kManyRowsPerSm * device_sm_count() && p.H <= 4096) {
+  if (p.T >= kManyRowsPerSm * device_sm_count() && p.H <= 2048) {
     if (p.H <= 1024) {
       const dim3 grid((p.T + 3) / 4), block(128);
       if (p.H <= 256) return launch_pdl(norm_warp_kernel<1>, grid, block, 0, s, p);
       if (p.H <= 512) return launch_pdl(norm_warp_kernel<2>, grid, block, 0, s, p);
       return launch_pdl(norm_warp_kernel<4>, grid, block, 0, s, p);
     }
-    if (p.H <= 2048) return launch_rows<2, 128, 12>(p, s);
-    if (p.H <= 2944) return launch_rows<3, 128, 8>(p, s);
-    return launch_rows<4, 128, 8>(p, s);
+    return launch_rows<2, 128, 12>(p, s);
   }
   if (p.H <= 2048) return launch_rows<1, 256, 8>(p, s);
   if (p.H <= 8192) return launch_rows<2, 512, 3>(p, s);

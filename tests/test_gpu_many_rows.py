@@ -14,8 +14,8 @@ from oracle import bf16, dense
 from test_gpu_norm import _bits, _check_backward, _dev, _inputs
 
 pytestmark = pytest.mark.gpu
-# the warp kernels (1, 2 and 4 words a lane) and the three block kernels, at their borders and between
-WIDTHS = [8, 96, 256, 264, 512, 520, 1000, 1024, 1032, 2048, 2056, 2880, 2944, 2952, 4096]
+# the warp kernels (1, 2 and 4 words a lane) and the block kernels, at their borders and between
+WIDTHS = [8, 96, 256, 264, 512, 520, 1000, 1024, 1032, 2048, 2056, 2880, 2976, 3064, 3200, 4096]
 
 
 def _rows(T):
