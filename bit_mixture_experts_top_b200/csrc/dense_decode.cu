@@ -1,6 +1,6 @@
 // The gated feed-forward block for a few tokens: the products are bound by the
-// weight stream, so every weight is read once, straight from global memory
-// into the registers of a warp-level MMA, with no shared-memory stage.
+// weight stream, so every weight is read once, by asynchronous copies into
+// shared memory that its own warp feeds to warp-level MMAs.
 //
 //   gate_up : h = act(x W_gate^T + b, x W_up^T + b)      8 features per block
 //   down    : out = h W_dn^T (+ b) (+ add)               16 rows per block

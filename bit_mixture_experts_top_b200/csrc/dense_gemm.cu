@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int B_ROWS = BN / CG;                      // this CTA's share of B
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 196608 / STAGE_BYTES;         // 4, 6 or 8 (pairs: 6)
+  static constexpr int STAGES = 196608 / STAGE_BYTES;         // 4 (one CTA of 256 columns) or 6
   static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // + slack to align the base
@@ -237,7 +237,6 @@ __device__ __forceinline__ uint4 finish_linear(const Params& p, int row, bool ro
   return pack8(f);
 }
 
-// All lanes of the warp call it with rows row0 + lane (row0 a multiple of 32).
 // G of eight columns, loaded ahead of its use.
 struct SavedG {
   float g[8], u[8];
@@ -250,6 +249,7 @@ struct SavedG {
   }
 };
 
+// All lanes of the warp call it with rows row0 + lane (row0 a multiple of 32).
 __device__ __forceinline__ void finish_dact(const Params& p, int row, bool row_in, int col, int lane, const SavedG& G,
                                             const float (&dh)[8], uint4& og, uint4& ou) {
   float dg[8], du[8];

@@ -91,7 +91,7 @@ class Grad(ctypes.Structure):
 
 def make_grads(grads, out=None):
     """The e4b_grad array of contiguous gradient tensors and of the tensors their clipped values go to (out None:
-    clipped in place); the tensors are kept alive with the array."""
+    clipped in place); the tensors are kept alive with the array, which names the addresses they have now."""
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):

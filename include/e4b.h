@@ -395,7 +395,8 @@ size_t e4b_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H);
 /*
  * Gradients of the norm.  With xh = r * rstd and c = mean over H of dy * weight * xh:
  *   dx = rstd * (dy * weight - xh * c) (+ dr), the gradient of x and of residual alike,
- *   dweight = sum over rows of dy * xh (the same bits for the same inputs).
+ *   dweight = sum over rows of dy * xh (the same bits for the same inputs),
+ * c and dweight summed in fp32.
  *   dy      : [T, H], dy_type E4B_F32 (e4b_moe_backward's dx) or E4B_BF16  (device, read)
  *   dr      : [T, H] bf16, the gradient that reaches r_out directly, or NULL (device, read)
  *   r, rstd : the forward's stream [T, H] bf16 and [T] fp32              (device, read)
@@ -430,7 +431,9 @@ size_t e4b_ffn_workspace_bytes(const e4b_ffn_desc* d, int32_t T);
 size_t e4b_ffn_train_workspace_bytes(const e4b_ffn_desc* d, int32_t T);
 
 /*
- * Forward of the gated feed-forward block; fp32 accumulation and epilogues.
+ * Forward of the gated feed-forward block; fp32 accumulation and epilogues (the
+ * activations use the fast exponential and quotient, 2^-18 of the value; a
+ * tensor-core sum of K products that rounds ends short by about 1e-9 K of it).
  *   x       : [T, H] bf16                                     (device, read)
  *   w_gu    : [2I, H] bf16, gate rows 0..I-1 then up rows     (device, read)
  *   w_dn    : [H, I] bf16                                     (device, read)
@@ -458,7 +461,7 @@ e4b_status e4b_ffn_forward_train(const e4b_ffn_desc* d, int32_t T, const uint16_
  * e4b_ffn_forward_train on this workspace (same desc, T, x and weights):
  *   dh = dout W_dn;  dG = act'(G) applied to dh (bf16 operand of what follows);
  *   dx = dG W_gu;  dw_gu = dG^T x;  dw_dn = dout^T h;
- *   dgu_bias = column sums of dG (before its rounding), ddn_bias of dout.
+ *   dgu_bias = column sums of dG (before its rounding), ddn_bias of dout, in fp32.
  *   dout     : [T, H] bf16, 16-byte aligned; the gradient of add is dout itself
  *   dx       : [T, H] bf16;  dw_gu : [2I, H] bf16;  dw_dn : [H, I] bf16
  *   dgu_bias : [2I] fp32;    ddn_bias : [H] fp32    (device, written)
