@@ -43,7 +43,7 @@ constexpr uint64_t kDrainNs = 50000000ull;
 // of it per product, measured over K of 256 to 12288 on zero-mean and on positive
 // data.  Nothing is put back: a factor would be wrong for every sum that was
 // exact (a gate exactly on the clamp would fall outside).  The split kernel, whose
-// tensor memory has room, lets several short chains meet in rounded additions
+// tensor memory has room, lets two shorter chains meet in a rounded addition
 // where an fp32 result leaves the kernel; the tiled kernels, whose two accumulators
 // fill the tensor memory, keep one chain (bias gradients 2.6e-6 off at 1500 tokens,
 // 4.3e-6 at 4096 with K = 2048, 6.1e-6 at 3000 with K = 2880).
@@ -528,11 +528,11 @@ struct SplitCfg {
   static constexpr int OFF_MISC = OFF_BAR + (2 * MAX_STAGES + 1) * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int EPI = 8, THREADS = 32 * (WARP_EPI0 + EPI);
-  // G and dh, whose fp32 values are kept or summed up, are accumulated in four chains of a quarter of the CTA's K,
-  // added in fp32 with rounding: the gate and up bias gradients of 509 x 2048 x 768 are 3.8e-7 off instead of 1.5e-6
-  // (relative 2-norm), for no more time.  What leaves as bf16 alone does not see it.
+  // G and dh, whose fp32 values are kept or summed up, are accumulated in two chains of half of the CTA's K, added in
+  // fp32 with rounding: the gate and up bias gradients of 509 x 2048 x 768 are 7.5e-7 off instead of 1.5e-6 (relative
+  // 2-norm) for 0.1 us a launch; four chains bring 3.8e-7 for 0.4.  What leaves as bf16 alone does not see it.
   template <int E>
-  static constexpr int chains() { return E == kEpiLinear ? 1 : 4; }
+  static constexpr int chains() { return E == kEpiLinear ? 1 : 2; }
   static_assert(OFF_SUMS + EPI * 2 * BN * 4 <= RING_BYTES, "both reuse the stages");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };

@@ -81,3 +81,16 @@ def test_two_streams_at_once(name):
     torch.cuda.synchronize()
     for w, outs in zip(want, got):
         assert all(torch.equal(o, w) for o in outs)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_no_tokens(name):
+    s = Setup(W[name], 4)
+    x = s.d["x"][:0]
+    out, r = s.block.forward(x, x)
+    assert out.shape == r.shape == x.shape
+    out, r, saved = s.block.forward_train(x, x)
+    got = s.block.backward(saved, x, x, router_grad=lambda dl: dl @ s.d["rw"].float())
+    assert got["dx"].shape == x.shape and got["dlogits"].shape == (0, s.w.E)
+    for k in ("norm", "gate_up", "down", "lora_A", "lora_B"):
+        assert got[k] is None or not got[k].any(), k
