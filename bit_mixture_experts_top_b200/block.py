@@ -62,6 +62,11 @@ def _lend(stream, index, *tensors):
             t.record_stream(torch.cuda.current_stream(index))
 
 
+def _same_desc(saved, own, what):
+    if saved is not own and bytes(saved) != bytes(own):
+        raise ValueError(f"e4b: the saved state is not of this {what}'s sizes and options")
+
+
 def check_waits(device=None):
     """Synchronises the device's current stream and raises E4BError if a bounded wait of any call on that device, graph
     replays among them, has run out since the last check: what those calls wrote is not to be trusted."""
@@ -153,8 +158,8 @@ class FfnSaved:
     before the backward) and the workspace with the pre-activations and h, whose scratch one backward at a time
     uses."""
 
-    def __init__(self, x, ws, stream):
-        self.x, self.ws, self.stream = x, ws, stream
+    def __init__(self, x, ws, stream, desc):
+        self.x, self.ws, self.stream, self.desc = x, ws, stream, desc
 
 
 class GluFfn:
@@ -208,11 +213,12 @@ class GluFfn:
     def forward_train(self, x, add=None, out=None):
         """(out, saved): the forward, and what :meth:`backward` needs of it."""
         out, ws = self._run("e4b_ffn_forward_train", e4b.e4b_ffn_train_workspace_bytes, x, add, out)
-        return out, FfnSaved(x, ws, _raw_stream(self.index))
+        return out, FfnSaved(x, ws, _raw_stream(self.index), self.desc)
 
     def backward(self, saved, dout, weights=True):
         """(dx, d_gate_up, d_down, d_gu_bias, d_dn_bias) of sum(dout * out): bf16, the biases' fp32 (None without them).
         The gradient of add is dout.  weights False: the weights are frozen and only dx is computed, the others None."""
+        _same_desc(saved.desc, self.desc, "feed-forward block")
         T = saved.x.shape[0]
         _check(dout, "dout", (T, self.H), torch.bfloat16)
         with _on(self.index, saved.x, dout):
@@ -257,7 +263,7 @@ class MoeBlock:
 
     def forward_train(self, x, residual=None):
         """(out, r, saved): the forward with what :meth:`backward` needs, the routed layer's workspace among it, so other
-        calls may come between a forward_train and its backward."""
+        calls may come between a forward_train and its backward (one backward of a saved state at a time)."""
         with _on(self.norm.index, x, residual):
             y, r, rstd = self.norm.forward_train(x, residual)
             logits = self._logits(y)
@@ -266,14 +272,15 @@ class MoeBlock:
             kept = None
             if self.shared is not None:
                 out, kept = self.shared.forward_train(y, add=out, out=out)
-            return out, r, (y, r, rstd, logits, kept, ws, _raw_stream(self.norm.index))
+            return out, r, (y, r, rstd, logits, kept, ws, _raw_stream(self.norm.index), self.moe.desc)
 
     def backward(self, saved, dout, dr=None, router_grad=None, weights=True):
         """Gradients of sum(dout * out) + sum(dr * r) as a dict: dx [T, H] bf16 (of x and residual alike), norm [H]
         fp32, dlogits [T, E] fp32, lora_A / lora_B fp32 (None without LoRA) and, with a shared expert, gate_up, down,
         gu_bias and dn_bias (None where frozen or absent).  router_grad: a callable dlogits -> its part of dy [T, H],
         the router's own backward; None leaves the router's path out of dx."""
-        y, r, rstd, logits, kept, ws, stream = saved
+        y, r, rstd, logits, kept, ws, stream, desc = saved
+        _same_desc(desc, self.moe.desc, "routed layer")
         _check(dout, "dout", y.shape, torch.bfloat16)
         with _on(self.norm.index, dout, dr):
             _lend(stream, self.norm.index, y, r, rstd, logits, ws)

@@ -82,3 +82,34 @@ def test_parts_on_different_devices_are_refused():
         H, index = FakeNorm().H, 1
     with pytest.raises(ValueError, match="device"):
         block.MoeBlock(FakeNorm(), None, moe, FakeShared())
+
+
+def test_saved_state_of_another_layer_is_refused(blk, monkeypatch):
+    # its routing and row counts would be read as this layer's
+    _, _, saved = blk.forward_train(_x(6))
+    stack = lambda e, n, k: layer.PackedStack(torch.empty(1), torch.empty(1), e, n, k, "nf4")  # noqa: E731
+    same = layer.MoeLayer(E, H, I, K, "nf4", stack(E, 2 * I, H), stack(E, H, I))
+    block.MoeBlock(blk.norm, blk.router, same).backward(saved, _x(6))
+    assert len(blk.reached) == 1
+    for e, i, k in ((4, I, K), (E, 2 * I, K), (E, I, 1)):
+        other = layer.MoeLayer(e, H, i, k, "nf4", stack(e, 2 * i, H), stack(e, H, i))
+        with pytest.raises(ValueError, match="saved"):
+            block.MoeBlock(blk.norm, blk.router, other).backward(saved, _x(6))
+    assert len(blk.reached) == 1
+
+
+def test_saved_state_of_another_feed_forward_block_is_refused(monkeypatch):
+    monkeypatch.setattr(block, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(block, "_on", lambda index, *t: contextlib.nullcontext())
+    reached = []
+    monkeypatch.setattr(e4b, "e4b_ffn_backward", lambda *a: reached.append(a))
+    z = lambda *s: _claims(torch.zeros(s, dtype=torch.bfloat16))  # noqa: E731
+    make = lambda h, i, glu=None: block.GluFfn(z(2 * i, h), z(h, i), glu=glu)  # noqa: E731
+    ffn = make(64, 128)
+    saved = block.FfnSaved(z(5, 64), torch.empty(1), 0, ffn.desc)
+    make(64, 128).backward(saved, z(5, 64))
+    assert len(reached) == 1
+    for other in (make(64, 256), make(128, 128), make(64, 128, (1.702, 7.0, 1.0))):
+        with pytest.raises(ValueError, match="saved"):
+            other.backward(saved, z(5, other.H))
+    assert len(reached) == 1
