@@ -45,7 +45,7 @@ constexpr uint64_t kDrainNs = 50000000ull;
 // exact (a gate exactly on the clamp would fall outside).  The split kernel, whose
 // tensor memory has room, lets two shorter chains meet in a rounded addition
 // where an fp32 result leaves the kernel; the tiled kernels, whose two accumulators
-// fill the tensor memory, keep one chain (bias gradients 2.6e-6 off at 1500 tokens,
+// fill the tensor memory, keep one chain (bias gradients 2.8e-6 off at 1500 tokens,
 // 4.3e-6 at 4096 with K = 2048, 6.1e-6 at 3000 with K = 2880).
 constexpr int kGroupM = 16;              // row tiles that share a sweep over the columns (L2 reuse of both operands)
 
